@@ -41,6 +41,10 @@
  *                 w = s * E4M3(c).  (The pages fix no block rule for their
  *                 FP8 weights; per-row 128-blocks also carry per-channel and
  *                 128x128-block scales.)
+ *  - QGEMM_INT8:  int8 c[N][K] and one fp32 scale t[N] per channel;  w = t * c.
+ *                 Any K <= 131071.  The activations are 8-bit codes too, one
+ *                 fp32 scale per row (qgemm_quantize_rows), so the whole sum
+ *                 over k is one of whole numbers, exact in 32 bits.
  *  E2M1 code bits: sign (bit 3), exponent (bits 2-1, bias 1), mantissa (bit 0):
  *  magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
  */
@@ -67,7 +71,8 @@ typedef enum qgemm_format {
     QGEMM_Q8_0 = 0,
     QGEMM_MXFP4 = 1,
     QGEMM_NVFP4 = 2,
-    QGEMM_FP8 = 3
+    QGEMM_FP8 = 3,
+    QGEMM_INT8 = 4
 } qgemm_format;
 
 typedef enum qgemm_dtype {
@@ -95,7 +100,14 @@ typedef enum qgemm_math {
      * weights are exact in bf16; a Q8_0 weight d*q or an FP8 weight s*E4M3(c)
      * is rounded once to bf16 in the large-batch tier.  Relative Frobenius
      * error <= 1e-2. */
-    QGEMM_MATH_BF16 = 1
+    QGEMM_MATH_BF16 = 1,
+    /* 8-bit activations: the math of QGEMM_INT8 weights, and of them only.
+     *     y[b][n] = fp32(sum_k q[b][k] c[n][k]) * s[b] * t[n]
+     * with q, s as qgemm_quantize_rows makes them.  The sum is exact and the
+     * result three fp32 roundings away from it (then SwiGLU and the output's
+     * rounding), whatever the tier, the batch width or the K split: a row's
+     * bits depend on that row alone. */
+    QGEMM_MATH_INT8 = 2
 } qgemm_math;
 
 /* Tiers (how a call maps onto kernels); qgemm_create flags may force one. */
@@ -140,6 +152,8 @@ typedef enum qgemm_tier {
  *      FP8  : byte 8u + j is the E4M3 code, as for Q8_0;
  *      FP4  : byte 4u + j holds the codes of k = ... + 2j (low nibble) and
  *             ... + 2j + 1 (high nibble), u = 0..3.
+ *    INT8 differs: KS = 64, K padded to a multiple of 128, and chunk L holds
+ *    the sixteen codes k = s*KS + 16g + 0..15 of row r in order.
  * 2. Scales: at a QGEMM_ALIGN-rounded offset, one record per slab, in the
  *    codes' order: record (rt, s) is at ((rt * S) + s) * 16 * E and its bytes
  *    E*r .. E*r+E-1 hold row r's scales of the slab, blocks in k order:
@@ -148,6 +162,7 @@ typedef enum qgemm_tier {
  *      NVFP4: E = 8, 8 E4M3 bytes (one per 16 weights);
  *      FP8  : E = 4, the fp32 scale of the 128-wide block holding the slab
  *             (each block's scale appears in both of its slabs' records).
+ *    INT8: instead one fp32 scale per row, Np of them in row order.
  * 3. NVFP4 only, at the next QGEMM_ALIGN offset, 256 bytes:
  *      int32 ntensors, int32 rows_per_tensor, int32 0, int32 0,
  *      float g[QGEMM_MAX_TENSORS];  row n uses g[n / rows_per_tensor].
@@ -162,11 +177,17 @@ size_t qgemm_weight_bytes(qgemm_format fmt, int64_t N, int64_t K);
  * pointer, out_bytes >= qgemm_weight_bytes).  codes: Q8_0 int8 [N][K]; FP4
  * uint8 [N][K], one code (0..15) per byte; FP8 uint8 [N][K] E4M3 codes.
  * scales: Q8_0 uint16 fp16 bits [N][K/32]; MXFP4 uint8 [N][K/32]; NVFP4
- * uint8 [N][K/16]; FP8 float [N][ceil(K/128)].  tensor_scales:
+ * uint8 [N][K/16]; FP8 float [N][ceil(K/128)]; INT8 (int8 codes) float [N].  tensor_scales:
  * NVFP4 only, ntensors (1..QGEMM_MAX_TENSORS, dividing N) fp32 values; NULL
  * and 0 for the other formats.  Pure host code, callable without a GPU. */
 int qgemm_pack(qgemm_format fmt, int64_t N, int64_t K, const void *codes, const void *scales,
                const float *tensor_scales, int64_t ntensors, void *out, size_t out_bytes);
+
+/* qgemm_pack on the device, for QGEMM_INT8 (QGEMM_ENOTSUP otherwise): codes
+ * int8 [N][K], scales float [N] and out are device pointers (out 16-byte
+ * aligned), the same bytes as qgemm_pack's. */
+int qgemm_pack_device(qgemm_format fmt, int64_t N, int64_t K, const void *codes, const void *scales, void *out,
+                      size_t out_bytes, void *stream);
 
 /* ------------------------------------------------------------------ plan */
 typedef struct qgemm_plan qgemm_plan;
@@ -174,7 +195,8 @@ typedef struct qgemm_plan qgemm_plan;
 /* Validate and record a problem shape: 1 <= N <= 2^30, 1 <= K <= 2^20, K a
  * multiple of the format's block.  act: activation dtype; out: output
  * dtype; math: see qgemm_math (QGEMM_MATH_FP32 needs act = QGEMM_F32; the
- * SwiGLU epilogue needs QGEMM_MATH_BF16, else QGEMM_ENOTSUP); flags:
+ * SwiGLU epilogue needs QGEMM_MATH_BF16, else QGEMM_ENOTSUP; QGEMM_INT8 weights
+ * take QGEMM_MATH_INT8, any act and epilogue, and K <= 131071); flags:
  * 0 or one QGEMM_FLAG_FORCE_* bit (also settable with the environment
  * variable QGEMM_FORCE_TIER=skinny|tiled|gemv).  Host-only: allocates the small
  * plan object, makes no HIP call and works without a device.  Tuning
@@ -191,6 +213,9 @@ int qgemm_create(qgemm_plan **plan, qgemm_format fmt, qgemm_dtype act, qgemm_dty
  *   x: activations [B][K] row-major (device, 16-byte aligned, act dtype);
  *   y: output [B][N] (or [B][N/2] for SwiGLU) row-major (device, out dtype);
  *      must not overlap x or w.
+ * A QGEMM_INT8 plan quantises x into a workspace first, so it runs through
+ * qgemm_run_ws and qgemm_run_noalloc (or qgemm_run_codes, without) and
+ * returns QGEMM_ENOTSUP here.
  * Any B >= 0; B = 0 returns QGEMM_OK and enqueues nothing.  No allocation,
  * no synchronisation.  Plans are immutable, so several threads may run one
  * plan at once.  Results are deterministic: no atomics, fixed summation order
@@ -223,7 +248,8 @@ int qgemm_run(const qgemm_plan *plan, int64_t B, const void *w, const void *x, v
  *     unsplit, so each expert's rows are bitwise those of qgemm_run of that
  *     expert in the large-batch tier without a workspace.
  * A plan forced to the GEMV tier, or to the small-batch tier with fp32 math,
- * returns QGEMM_ENOTSUP.  T = 0 returns QGEMM_OK and enqueues nothing.
+ * or of QGEMM_INT8 weights (qgemm_run_grouped_codes), returns
+ * QGEMM_ENOTSUP.  T = 0 returns QGEMM_OK and enqueues nothing.
  * The offsets are read and checked on the device: when they break a rule
  * above, the kernel reads and writes nothing outside the offsets array and
  * the table and sets QGEMM_DEV_BAD_OFFSETS in the device status word (y is
@@ -309,6 +335,7 @@ int qgemm_xcd_local(void);
 /* Device status word bits: conditions a kernel detected while it ran. */
 #define QGEMM_DEV_XCD_MISMATCH 0x1u /* the K splits of a row group ran on different XCDs */
 #define QGEMM_DEV_BAD_OFFSETS 0x2u  /* qgemm_run_grouped offsets broke their rules; no work done */
+#define QGEMM_DEV_BAD_ROUTE 0x4u    /* a position of a sorted row was past the rows; treated as dropped */
 
 /* Read the current device's status word into *bits (the OR of every bit set
  * since it was last cleared), after synchronising `stream` (the word is set
@@ -317,13 +344,93 @@ int qgemm_xcd_local(void);
  * capture. */
 int qgemm_device_status(uint32_t *bits, int clear, void *stream);
 
+/* ------------------------------------------------- 8-bit rows and products
+ * Rows of 8-bit codes: int8 [B][ldc] with ldc bytes from row to row (ldc >= K,
+ * a multiple of 16, at most 2^21; the buffer holds B * ldc bytes, 16-byte
+ * aligned) and fp32 scales [B].  Bytes K .. ldc-1 of a row are written as zero
+ * and read, but never matter. */
+
+/* x [B][K] (act: QGEMM_F32 or QGEMM_BF16, row-major, 16-byte aligned) to codes:
+ *     s[b] = fp32(max_k |x[b][k]| / 127),
+ *     q[b][k] = clamp(round_half_even(fp32(x[b][k] / s[b])), -127, 127),
+ * both quotients correctly rounded.  A row of zeros (or one so small that its
+ * scale underflows) gets s = 0 and codes 0; a row that holds a NaN or an
+ * infinity gets s = NaN and codes 0, so its products are NaN.  1 <= K <= 2^20;
+ * B = 0 is a no-op. */
+int qgemm_quantize_rows(qgemm_dtype act, int64_t B, int64_t K, const void *x, int8_t *codes, int64_t ldc,
+                        float *scales, void *stream);
+
+/* y = the QGEMM_INT8 product (or its SwiGLU) for B rows of codes; w and y as
+ * in qgemm_run.  workspace: as in qgemm_run_ws, at least
+ * qgemm_workspace_bytes(plan, B) bytes to let the large-batch tier split K
+ * (that size covers the rows of qgemm_run_ws too), else NULL; the counter
+ * region is left alone and the rest need not be zeroed.  The result's bits do
+ * not depend on it. */
+int qgemm_run_codes(const qgemm_plan *plan, int64_t B, const void *w, const int8_t *codes, int64_t ldc,
+                    const float *scales, void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Routed experts with QGEMM_INT8 weights: as qgemm_run_grouped with rows of
+ * codes, except that offsets[E] may be below T: rows from offsets[E] on are
+ * neither read nor written (qgemm_route leaves such rows when it drops
+ * choices).  An expert whose own two offsets are out of order or outside 0..T
+ * is left out and sets QGEMM_DEV_BAD_OFFSETS; y is then not to be trusted.
+ * qgemm_grouped_tier tells the route; each expert's rows are bitwise those of
+ * qgemm_run_codes on them, on either. */
+int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const void *const *w_table,
+                            const int32_t *offsets, const int8_t *codes, int64_t ldc, const float *scales, void *y,
+                            void *stream);
+
+/* --------------------------------------------------- rows sorted by expert
+ * What stands before and after the routed experts: T tokens that each chose
+ * topk (1..QGEMM_MAX_TOPK) of E experts.  The choice j of token t has the flat
+ * index t * topk + j.  A choice is dropped when its id is outside 0..E-1 (an
+ * expert held elsewhere, a padding token): it has no row, counts nothing and
+ * gets no gradient.  The same expert may be chosen twice.  Rows are row-major
+ * without gaps, QGEMM_F32 or QGEMM_BF16, 16-byte aligned; inputs and outputs
+ * must not overlap.  T = 0 is a no-op (qgemm_route then writes zero offsets).
+ * Results are deterministic. */
+#define QGEMM_MAX_TOPK 64
+
+/* ids [T][topk] (device int32) -> offsets [E + 1], those that the routed
+ * products take (offsets[E] = choices kept), and pos [T][topk]: the sorted row
+ * of each choice, -1 for a dropped one.  Stable: the rows of an expert are in
+ * flat order.  E above 16384 returns QGEMM_ENOTSUP. */
+int qgemm_route(int64_t E, int64_t T, int64_t topk, const int32_t *ids, int32_t *offsets, int32_t *pos, void *stream);
+
+/* xs[pos[t][j]] = x[t]: x [T][H] to the sorted rows xs [R][H].  Rows that no
+ * choice names are left as they were.  Positions are read on the device: one
+ * of R or more is treated as dropped and sets QGEMM_DEV_BAD_ROUTE. */
+int qgemm_dispatch(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *x, const int32_t *pos,
+                   void *xs, void *stream);
+
+/* qgemm_quantize_rows and qgemm_dispatch in one: each row of x [T][K] is read
+ * once, and its codes and scale written to its sorted rows of codes [R][ldc]
+ * and scales [R]. */
+int qgemm_dispatch_codes(qgemm_dtype act, int64_t T, int64_t topk, int64_t K, int64_t R, const void *x,
+                         const int32_t *pos, int8_t *codes, int64_t ldc, float *scales, void *stream);
+
+/* y[t] = sum_j weights[t][j] * ys[pos[t][j]]: the sorted rows ys [R][H] back
+ * to y [T][H], summed in fp32 in the order of j and rounded once; a token
+ * with every choice dropped gets zeros.  weights: fp32 [T][topk], or NULL for
+ * ones, which makes this the gradient of qgemm_dispatch (ys = the gradient of
+ * xs). */
+int qgemm_combine(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *ys, const int32_t *pos,
+                  const float *weights, void *y, void *stream);
+
+/* The gradient of qgemm_combine, from dy [T][H]:
+ *     dys[pos[t][j]] = weights[t][j] * dy[t]   (rounded to dt; rows that no
+ *                      choice names are left as they were),
+ *     dw[t][j] = sum_h dy[t][h] * ys[pos[t][j]][h]   (fp32; 0 when dropped). */
+int qgemm_combine_grad(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *dy, const void *ys,
+                       const int32_t *pos, const float *weights, void *dys, float *dw, void *stream);
+
 /* Release a plan (NULL is accepted). */
 int qgemm_destroy(qgemm_plan *plan);
 
 /* Device decode of a packed buffer to fp32 w_out[N][K] (device pointer),
  * using the kernels' own decoders: Q8_0 d*q; MXFP4 E2M1 * 2^(e-127); NVFP4
- * g * (E2M1 * E4M3) rounded once to fp32; FP8 s * E4M3(c) rounded once to
- * fp32.  Every other value is exact. */
+ * g * (E2M1 * E4M3) rounded once to fp32; FP8 s * E4M3(c) and INT8 t * c
+ * rounded once to fp32.  Every other value is exact. */
 int qgemm_dequantize(qgemm_format fmt, const void *w, float *w_out, int64_t N, int64_t K,
                      void *stream);
 

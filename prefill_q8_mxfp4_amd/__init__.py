@@ -24,10 +24,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("QGEMM_LIB_PATH") or os.path.join(_HERE, "libqgemm.so")
 
 OK, EINVAL, ENOTSUP, EHIP, ENOMEM = 0, 1, 2, 3, 4
-FORMATS = {"q8_0": 0, "mxfp4": 1, "nvfp4": 2, "fp8": 3}
+FORMATS = {"q8_0": 0, "mxfp4": 1, "nvfp4": 2, "fp8": 3, "int8": 4}
 DTYPES = {"f32": 0, "bf16": 1}
 EPILOGUES = {"none": 0, "swiglu": 1}
-MATHS = {"fp32": 0, "bf16": 1}
+MATHS = {"fp32": 0, "bf16": 1, "int8": 2}
 TIERS = {1: "skinny", 2: "tiled", 3: "gemv"}
 FLAG_FORCE_SKINNY = 0x1
 FLAG_FORCE_TILED = 0x2
@@ -41,9 +41,13 @@ EXPORTS = ("qgemm_weight_bytes", "qgemm_pack", "qgemm_create", "qgemm_run", "qge
            "qgemm_device_status",
            "qgemm_destroy", "qgemm_dequantize", "qgemm_read_bytes", "qgemm_mfma_rate", "qgemm_strerror",
            "qgemm_last_error",
-           "qgemm_version")
+           "qgemm_version",
+           "qgemm_pack_device", "qgemm_quantize_rows", "qgemm_run_codes", "qgemm_run_grouped_codes",
+           "qgemm_route", "qgemm_dispatch", "qgemm_dispatch_codes", "qgemm_combine", "qgemm_combine_grad")
 DEV_XCD_MISMATCH = 0x1
 DEV_BAD_OFFSETS = 0x2
+DEV_BAD_ROUTE = 0x4
+MAX_TOPK = 64                     # QGEMM_MAX_TOPK
 SCRATCH_BYTES = 64 << 20          # QGEMM_SCRATCH_BYTES
 SCRATCH_COUNTER_BYTES = 1 << 20   # QGEMM_SCRATCH_COUNTER_BYTES
 
@@ -107,6 +111,24 @@ def lib():
     L.qgemm_init_device.argtypes = []
     L.qgemm_device_status.restype = i32
     L.qgemm_device_status.argtypes = [ctypes.POINTER(u32), i32, vp]
+    L.qgemm_pack_device.restype = i32
+    L.qgemm_pack_device.argtypes = [i32, i64, i64, vp, vp, vp, sz, vp]
+    L.qgemm_quantize_rows.restype = i32
+    L.qgemm_quantize_rows.argtypes = [i32, i64, i64, vp, vp, i64, vp, vp]
+    L.qgemm_run_codes.restype = i32
+    L.qgemm_run_codes.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, sz, vp]
+    L.qgemm_run_grouped_codes.restype = i32
+    L.qgemm_run_grouped_codes.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp]
+    L.qgemm_route.restype = i32
+    L.qgemm_route.argtypes = [i64, i64, i64, vp, vp, vp, vp]
+    L.qgemm_dispatch.restype = i32
+    L.qgemm_dispatch.argtypes = [i32, i64, i64, i64, i64, vp, vp, vp, vp]
+    L.qgemm_dispatch_codes.restype = i32
+    L.qgemm_dispatch_codes.argtypes = [i32, i64, i64, i64, i64, vp, vp, vp, i64, vp, vp]
+    L.qgemm_combine.restype = i32
+    L.qgemm_combine.argtypes = [i32, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.qgemm_combine_grad.restype = i32
+    L.qgemm_combine_grad.argtypes = [i32, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
     _lib = L
     return L
 
@@ -154,17 +176,19 @@ def pack(fmt: str, N: int, K: int, codes: np.ndarray, scales: np.ndarray, g=None
     codes: Q8_0 int8 [N][K]; FP4 uint8 [N][K] (one code per byte); FP8 uint8
     [N][K] E4M3 codes.
     scales: Q8_0 uint16 fp16 bits [N][K/32]; MXFP4 uint8 [N][K/32]; NVFP4 uint8 [N][K/16];
-    FP8 float32 [N][ceil(K/128)].
+    FP8 float32 [N][ceil(K/128)]; INT8 (int8 codes) float32 [N].
     g: NVFP4 tensor scales (1..60 fp32 values; rows split evenly among them).
     """
     codes = np.ascontiguousarray(codes)
     scales = np.ascontiguousarray(scales)
     if codes.shape != (N, K) or codes.itemsize != 1:
         raise QgemmError(EINVAL, f"codes must be one byte per weight, shape ({N}, {K})")
-    want = {"q8_0": (np.uint16, K // 32), "mxfp4": (np.uint8, K // 32),
-            "nvfp4": (np.uint8, K // 16), "fp8": (np.float32, -(-K // 128))}[fmt]
-    if scales.dtype != want[0] or scales.shape != (N, want[1]):
-        raise QgemmError(EINVAL, f"{fmt} scales must be {np.dtype(want[0]).name} [{N}][{want[1]}]")
+    want = {"q8_0": (np.uint16, (N, K // 32)), "mxfp4": (np.uint8, (N, K // 32)),
+            "nvfp4": (np.uint8, (N, K // 16)), "fp8": (np.float32, (N, -(-K // 128))),
+            "int8": (np.float32, (N,))}[fmt]
+    if scales.dtype != want[0] or scales.shape != want[1]:
+        raise QgemmError(EINVAL, f"{fmt} scales must be {np.dtype(want[0]).name} "
+                         + "".join(f"[{n}]" for n in want[1]))
     nbytes = weight_bytes(fmt, N, K)
     if nbytes == 0:
         raise QgemmError(EINVAL, f"bad shape for {fmt}: N={N} K={K}")
@@ -209,7 +233,7 @@ class Plan:
     def __init__(self, fmt: str, N: int, K: int, act: str = "bf16", out: str = "f32",
                  epilogue: str = "none", math: str | None = None, tier: str | None = None):
         if math is None:
-            math = "fp32" if act == "f32" else "bf16"
+            math = "int8" if fmt == "int8" else "fp32" if act == "f32" else "bf16"
         flags = 0
         if tier == "skinny":
             flags = FLAG_FORCE_SKINNY
@@ -260,7 +284,13 @@ class Plan:
             if old is not None and old.device == device and not torch.cuda.is_current_stream_capturing():
                 old.record_stream(stream)
             self._ws = ws
-        if not torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
+            # replays use this buffer for as long as the plan lives, also
+            # after a later call has taken a larger one
+            kept = self.__dict__.setdefault("_ws_captured", [])
+            if not any(k is ws for k in kept):
+                kept.append(ws)
+        else:
             ws.record_stream(stream)
         return ws
 
@@ -337,6 +367,50 @@ class Plan:
                                        _dev_ptr(y, "y"), _stream_ptr(stream)))
         return y
 
+    def run_codes(self, codes, scales, w, y, stream=None, workspace="auto"):
+        """qgemm_run_codes: y = the int8 product of rows that are codes
+        already (quantize_rows): codes int8 [B][K], rows 16-byte aligned at
+        any pitch; scales float32 [B].  workspace as in run()."""
+        import torch
+
+        B, ldc = _codes_pitch(codes, scales, self.K)
+        want_y = torch.float32 if self.out == "f32" else torch.bfloat16
+        if y.dtype != want_y or w.dtype != torch.uint8:
+            raise TypeError("dtype mismatch: w %s, y %s" % (w.dtype, y.dtype))
+        if y.numel() < B * self.out_cols:
+            raise ValueError("y too small for B")
+        if w.numel() < weight_bytes(self.fmt, self.N, self.K):
+            raise ValueError("packed weight buffer too small")
+        with _device_of(codes, scales, w, y) as dev:
+            st = torch.cuda.current_stream(codes.device) if stream is None else stream
+            if isinstance(workspace, str):
+                workspace = self._workspace(B, codes.device, st) if B > 0 else None
+            wsp, wsn = (0, 0) if workspace is None else (_dev_ptr(workspace, "workspace"), workspace.numel())
+            _check(lib().qgemm_run_codes(self._h, B, _dev_ptr(w, "w"), codes.data_ptr(), ldc,
+                                         _dev_ptr(scales, "scales"), _dev_ptr(y, "y"), wsp, wsn, st.cuda_stream))
+        return y
+
+    def run_grouped_codes(self, codes, scales, w_table, offsets, y, stream=None):
+        """qgemm_run_grouped_codes: routed experts on rows of codes sorted by
+        expert (route, dispatch_codes); w_table and offsets as in
+        run_grouped.  Rows from offsets[E] on are left as they were."""
+        import torch
+
+        T, ldc = _codes_pitch(codes, scales, self.K)
+        E = w_table.numel()
+        want_y = torch.float32 if self.out == "f32" else torch.bfloat16
+        if y.dtype != want_y:
+            raise TypeError("dtype mismatch: y %s" % y.dtype)
+        if w_table.dtype != torch.int64 or offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+            raise TypeError("w_table must be int64 [E], offsets int32 [E + 1]")
+        if y.numel() < T * self.out_cols:
+            raise ValueError("y too small")
+        with _device_of(codes, scales, w_table, offsets, y) as dev:
+            _check(lib().qgemm_run_grouped_codes(
+                self._h, E, T, _dev_ptr(w_table, "w_table"), _dev_ptr(offsets, "offsets"), codes.data_ptr(), ldc,
+                _dev_ptr(scales, "scales"), _dev_ptr(y, "y"), _raw_stream(stream, dev)))
+        return y
+
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
             lib().qgemm_destroy(self._h)
@@ -347,6 +421,237 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+class _device_of:
+    """The one device of the tensors, made the current one inside the block
+    (kernels, the status word and streams belong to it)."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, *tensors):
+        d = tensors[0].device
+        for t in tensors:
+            if t.device != d or d.type != "cuda":
+                raise ValueError("tensors must be on one CUDA (HIP) device")
+        self.index = d.index
+
+    def __enter__(self):
+        import torch
+
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return self.index
+
+    def __exit__(self, *exc):
+        import torch
+
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _raw_stream(stream, index):
+    import torch
+
+    return torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
+
+
+def code_stride(K: int) -> int:
+    """The pitch at which quantize_rows allocates rows of K codes."""
+    return (K + 15) // 16 * 16
+
+
+def _codes_pitch(codes, scales, K):
+    """(rows, pitch) of a tensor of codes, checked with its scales."""
+    import torch
+
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise TypeError("codes must be int8 and scales float32, not %s and %s" % (codes.dtype, scales.dtype))
+    if codes.dim() != 2 or codes.shape[1] != K:
+        raise ValueError("codes must be [rows][%d], not %s" % (K, tuple(codes.shape)))
+    B = codes.shape[0]
+    # one row, or none, carries no pitch of its own
+    ldc = codes.stride(0) if B > 1 else max(codes.stride(0), code_stride(K))
+    if (K > 1 and codes.stride(1) != 1) or ldc % 16 or ldc < K:
+        raise ValueError("codes must be rows of stride 1 at a pitch that is a multiple of 16 and at least K")
+    if B and codes.untyped_storage().nbytes() - codes.storage_offset() < B * ldc:
+        raise ValueError("the last row of codes must have room for its whole pitch (%d bytes)" % ldc)
+    if scales.numel() < B:
+        raise ValueError("scales too small")
+    return B, ldc
+
+
+def _rows_dtype(t, name):
+    import torch
+
+    if t.dtype == torch.float32:
+        return 0
+    if t.dtype == torch.bfloat16:
+        return 1
+    raise TypeError("%s must be float32 or bfloat16, not %s" % (name, t.dtype))
+
+
+def pack_int8(codes, scales, out=None, stream=None):
+    """qgemm_pack_device: int8 codes [N][K] and float32 scales [N] on the GPU
+    to the packed buffer (uint8, allocated unless given)."""
+    import torch
+
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise TypeError("codes must be int8 and scales float32, not %s and %s" % (codes.dtype, scales.dtype))
+    if codes.dim() != 2 or scales.shape != codes.shape[:1]:
+        raise ValueError("codes must be [N][K], scales [N]")
+    N, K = codes.shape
+    nbytes = weight_bytes("int8", N, K)
+    if out is None:
+        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    if out.dtype != torch.uint8 or out.numel() < nbytes:
+        raise ValueError("out must be uint8, at least %d bytes" % nbytes)
+    with _device_of(codes, scales, out) as dev:
+        _check(lib().qgemm_pack_device(FORMATS["int8"], N, K, _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"),
+                                       _dev_ptr(out, "out"), out.numel(), _raw_stream(stream, dev)))
+    return out
+
+
+def _new_codes(R, K, device):
+    import torch
+
+    return torch.empty((R, code_stride(K)), dtype=torch.int8, device=device)[:, :K]
+
+
+def quantize_rows(x, codes=None, scales=None, stream=None):
+    """qgemm_quantize_rows: float32 or bfloat16 rows x [B][K] to int8 codes
+    [B][K] (at a pitch of code_stride(K)) and float32 scales [B]; outputs are
+    allocated unless given."""
+    import torch
+
+    dt = _rows_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B][K]")
+    B, K = x.shape
+    if codes is None:
+        codes = _new_codes(B, K, x.device)
+    if scales is None:
+        scales = torch.empty(B, dtype=torch.float32, device=x.device)
+    rows, ldc = _codes_pitch(codes, scales, K)
+    if rows != B:
+        raise ValueError("codes must have x's rows")
+    with _device_of(x, codes, scales) as dev:
+        _check(lib().qgemm_quantize_rows(dt, B, K, _dev_ptr(x, "x"), codes.data_ptr(), ldc,
+                                         _dev_ptr(scales, "scales"), _raw_stream(stream, dev)))
+    return codes, scales
+
+
+def route(ids, E: int, offsets=None, pos=None, stream=None):
+    """qgemm_route: the router's choices ids (int32 [T][topk]; ids outside
+    0..E-1 are dropped) to the offsets (int32 [E + 1]) that run_grouped and
+    run_grouped_codes take and the sorted row of each choice, pos (int32
+    [T][topk], -1 for a dropped one); outputs are allocated unless given."""
+    import torch
+
+    if ids.dtype != torch.int32 or ids.dim() != 2:
+        raise TypeError("ids must be int32 [T][topk]")
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+    if pos is None:
+        pos = torch.empty_like(ids)
+    if offsets.dtype != torch.int32 or pos.dtype != torch.int32:
+        raise TypeError("offsets and pos must be int32")
+    if offsets.numel() != E + 1 or pos.shape != ids.shape:
+        raise ValueError("offsets must be [E + 1], pos as ids")
+    with _device_of(ids, offsets, pos) as dev:
+        _check(lib().qgemm_route(E, ids.shape[0], ids.shape[1], _dev_ptr(ids, "ids"), _dev_ptr(offsets, "offsets"),
+                                 _dev_ptr(pos, "pos"), _raw_stream(stream, dev)))
+    return offsets, pos
+
+
+def _check_pos(pos, T):
+    import torch
+
+    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != T:
+        raise TypeError("pos must be int32 [T][topk]")
+
+
+def _check_weights(weights, pos, name="weights"):
+    import torch
+
+    if weights.dtype != torch.float32 or weights.shape != pos.shape:
+        raise TypeError("%s must be float32 [T][topk]" % name)
+
+
+def _check_rows(rows, like, name):
+    if rows.dtype != like.dtype:
+        raise TypeError("dtype mismatch: %s %s" % (name, rows.dtype))
+    if rows.dim() != 2 or rows.shape[1] != like.shape[1]:
+        raise ValueError("%s must be rows of %d" % (name, like.shape[1]))
+
+
+def dispatch(x, pos, xs, stream=None):
+    """qgemm_dispatch: xs[pos[t][j]] = x[t], x [T][H] and xs [R][H] float32
+    or bfloat16.  Rows of xs that no choice names are left as they were."""
+    dt = _rows_dtype(x, "x")
+    _check_rows(xs, x, "xs")
+    _check_pos(pos, x.shape[0])
+    with _device_of(x, pos, xs) as dev:
+        _check(lib().qgemm_dispatch(dt, x.shape[0], pos.shape[1], x.shape[1], xs.shape[0], _dev_ptr(x, "x"),
+                                    _dev_ptr(pos, "pos"), _dev_ptr(xs, "xs"), _raw_stream(stream, dev)))
+    return xs
+
+
+def dispatch_codes(x, pos, codes, scales, stream=None):
+    """qgemm_dispatch_codes: quantize_rows and dispatch in one pass: x [T][K]
+    to the sorted rows of codes [R][K] and scales [R]."""
+    dt = _rows_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T][K]")
+    _check_pos(pos, x.shape[0])
+    R, ldc = _codes_pitch(codes, scales, x.shape[1])
+    with _device_of(x, pos, codes, scales) as dev:
+        _check(lib().qgemm_dispatch_codes(dt, x.shape[0], pos.shape[1], x.shape[1], R, _dev_ptr(x, "x"),
+                                          _dev_ptr(pos, "pos"), codes.data_ptr(), ldc, _dev_ptr(scales, "scales"),
+                                          _raw_stream(stream, dev)))
+    return codes, scales
+
+
+def combine(ys, pos, weights, y, stream=None):
+    """qgemm_combine: y[t] = sum_j weights[t][j] * ys[pos[t][j]], ys [R][H]
+    and y [T][H] float32 or bfloat16, weights float32 [T][topk] or None (ones)."""
+    dt = _rows_dtype(ys, "ys")
+    _check_rows(y, ys, "y")
+    _check_pos(pos, y.shape[0])
+    tensors = (ys, pos, y)
+    if weights is not None:
+        _check_weights(weights, pos)
+        tensors += (weights,)
+    with _device_of(*tensors) as dev:
+        _check(lib().qgemm_combine(dt, y.shape[0], pos.shape[1], y.shape[1], ys.shape[0], _dev_ptr(ys, "ys"),
+                                   _dev_ptr(pos, "pos"), None if weights is None else _dev_ptr(weights, "weights"),
+                                   _dev_ptr(y, "y"), _raw_stream(stream, dev)))
+    return y
+
+
+def dispatch_grad(dxs, pos, dx, stream=None):
+    """The gradient of dispatch: dx[t] = sum_j dxs[pos[t][j]]."""
+    return combine(dxs, pos, None, dx, stream)
+
+
+def combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
+    """qgemm_combine_grad: dys[pos[t][j]] = weights[t][j] * dy[t] and
+    dw[t][j] = dy[t] . ys[pos[t][j]] (float32, 0 for a dropped choice); rows
+    of dys that no choice names are left as they were."""
+    dt = _rows_dtype(dy, "dy")
+    _check_rows(ys, dy, "ys")
+    _check_rows(dys, dy, "dys")
+    _check_pos(pos, dy.shape[0])
+    _check_weights(weights, pos)
+    _check_weights(dw, pos, "dw")
+    if dys.shape[0] != ys.shape[0]:
+        raise ValueError("dys must have ys's rows")
+    with _device_of(dy, ys, pos, weights, dys, dw) as dev:
+        _check(lib().qgemm_combine_grad(dt, dy.shape[0], pos.shape[1], dy.shape[1], ys.shape[0], _dev_ptr(dy, "dy"),
+                                        _dev_ptr(ys, "ys"), _dev_ptr(pos, "pos"), _dev_ptr(weights, "weights"),
+                                        _dev_ptr(dys, "dys"), _dev_ptr(dw, "dw"), _raw_stream(stream, dev)))
+    return dys, dw
 
 
 def dequantize(fmt: str, w, N: int, K: int, stream=None):

@@ -10,7 +10,7 @@
 #include <mutex>
 #include <new>
 
-#include "common.h"
+#include "int8.h"
 
 namespace qg {
 
@@ -541,9 +541,20 @@ static int64_t skinny_ws_bytes(const Problem &p, int64_t B)
     return c.cnt_bytes + c.part_bytes;
 }
 
+// INT8 plans: the small kernel (weights straight into the operands) or the
+// tiled one; both give the same bits.
+static int i8_tier(const qgemm_plan *plan, int64_t B)
+{
+    if (plan->forced_tier)
+        return plan->forced_tier;
+    return B <= I8_SMALL_MAX_B ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
+}
+
 static int choose_tier(const qgemm_plan *plan, int64_t B)
 {
     const Problem &p = plan->p;
+    if (p.fmt == FMT_I8)
+        return i8_tier(plan, B);
     if (plan->forced_tier)
         return plan->forced_tier;
     if (use_gemv(p, B))  // B = 1, 2: the GEMV kernel (no K split, no workspace)
@@ -559,6 +570,43 @@ static int choose_tier(const qgemm_plan *plan, int64_t B)
     // on MI355X the tiled tier wins from B = 48 in every format (and at 32 for
     // MXFP4 and Q8_0).  Both give way to the verify kernel where it applies.
     return B <= 32 ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
+}
+
+static I8Args i8_args(const Problem &p, int64_t B, const void *w, const int8_t *codes, int64_t ldc, const float *xs,
+                      void *y)
+{
+    I8Args a;
+    a.w = (const uint8_t *)w;
+    a.codes = codes;
+    a.xs = xs;
+    a.y = y;
+    a.scale_off = p.L.scale_off;
+    a.B = (int)B;
+    a.N = (int)p.N;
+    a.K = (int)p.K;
+    a.S = (int)p.L.S;
+    a.RT = (int)p.L.RT;
+    a.Nh = p.epi == QGEMM_EPI_SWIGLU ? (int)(p.N / 2) : 0;
+    a.ncols = a.Nh ? a.Nh : a.N;
+    a.ldc = (int)ldc;
+    return a;
+}
+
+// Workspace of an INT8 call after the counters (which it leaves alone): the
+// int32 partial tiles of a K split, then the codes and scales of rows that come
+// as fp32 or bf16.
+static int64_t i8_part_bytes(const qgemm_plan *plan, int64_t B)
+{
+    if (i8_tier(plan, B) != QGEMM_TIER_TILED)
+        return 0;
+    return round_up(i8_tiled_cfg(i8_args(plan->p, B, nullptr, nullptr, 0, nullptr, nullptr), true).part_bytes, 256);
+}
+
+static int64_t i8_code_stride(const Problem &p) { return round_up(p.K, 16); }
+
+static int64_t i8_rows_bytes(const Problem &p, int64_t B)
+{
+    return round_up(B * i8_code_stride(p), 256) + round_up(B * 4, 256);
 }
 
 static KArgs make_args(const Problem &p, int64_t B, const void *w, const void *x, void *y)
@@ -634,6 +682,16 @@ int qgemm_pack(qgemm_format fmt, int64_t N, int64_t K, const void *codes, const 
     }
     uint8_t *o = (uint8_t *)out;
     memset(o, 0, (size_t)L.total);
+    if (fmt == QGEMM_INT8) {
+        for (int64_t n = 0; n < N; n++)
+            for (int64_t k = 0; k < K; k += 16) {
+                const int64_t s = k / L.KS, g = k % L.KS / 16;
+                memcpy(o + ((n / 16 * L.S + s) << 10) + ((g * 16 + n % 16) << 4), (const int8_t *)codes + n * K + k,
+                       (size_t)(K - k < 16 ? K - k : 16));
+            }
+        memcpy(o + L.scale_off, scales, (size_t)N * sizeof(float));
+        return QGEMM_OK;
+    }
     // codes
     for (int64_t n = 0; n < N; n++) {
         const int64_t rt = n / 16, r = n % 16;
@@ -687,14 +745,16 @@ int qgemm_create(qgemm_plan **plan, qgemm_format fmt, qgemm_dtype act, qgemm_dty
     if (!plan)
         return fail(QGEMM_EINVAL, "qgemm_create: null plan pointer");
     *plan = nullptr;
-    if ((int)fmt < 0 || (int)fmt > 3)
+    if ((int)fmt < 0 || (int)fmt > 4)
         return fail(QGEMM_EINVAL, "qgemm_create: unknown format %d", (int)fmt);
     if ((act != QGEMM_F32 && act != QGEMM_BF16) || (out != QGEMM_F32 && out != QGEMM_BF16))
         return fail(QGEMM_EINVAL, "qgemm_create: unknown dtype");
     if (epi != QGEMM_EPI_NONE && epi != QGEMM_EPI_SWIGLU)
         return fail(QGEMM_EINVAL, "qgemm_create: unknown epilogue %d", (int)epi);
-    if (math != QGEMM_MATH_FP32 && math != QGEMM_MATH_BF16)
+    if (math != QGEMM_MATH_FP32 && math != QGEMM_MATH_BF16 && math != QGEMM_MATH_INT8)
         return fail(QGEMM_EINVAL, "qgemm_create: unknown math mode %d", (int)math);
+    if ((fmt == QGEMM_INT8) != (math == QGEMM_MATH_INT8))
+        return fail(QGEMM_EINVAL, "qgemm_create: QGEMM_INT8 weights and QGEMM_MATH_INT8 go together");
     if (N <= 0 || K <= 0)
         return fail(QGEMM_EINVAL, "qgemm_create: N and K must be positive (N=%lld K=%lld)",
                     (long long)N, (long long)K);
@@ -702,7 +762,10 @@ int qgemm_create(qgemm_plan **plan, qgemm_format fmt, qgemm_dtype act, qgemm_dty
     // weight rows stay below 2^31 bytes, so the kernels' 32-bit offsets hold
     if (N > (1ll << 30) || K > (1ll << 20))
         return fail(QGEMM_EINVAL, "qgemm_create: N above 2^30 or K above 2^20");
-    const int64_t blk = fmt == QGEMM_NVFP4 ? 16 : 32;
+    if (fmt == QGEMM_INT8 && K > I8_MAX_K)
+        return fail(QGEMM_EINVAL, "qgemm_create: QGEMM_INT8 sums of K=%lld codes do not fit in 32 bits (K <= %lld)",
+                    (long long)K, (long long)I8_MAX_K);
+    const int64_t blk = block_of((int)fmt);
     if (K % blk)
         return fail(QGEMM_EINVAL, "qgemm_create: K=%lld is not a multiple of the %lld-wide block",
                     (long long)K, (long long)blk);
@@ -731,6 +794,8 @@ int qgemm_create(qgemm_plan **plan, qgemm_format fmt, qgemm_dtype act, qgemm_dty
         else if (e && !strcmp(e, "gemv"))
             forced = QGEMM_TIER_GEMV;
     }
+    if (fmt == QGEMM_INT8 && forced == QGEMM_TIER_GEMV)
+        return fail(QGEMM_ENOTSUP, "qgemm_create: QGEMM_INT8 has no GEMV tier");
     qgemm_plan *p = new (std::nothrow) qgemm_plan;
     if (!p)
         return fail(QGEMM_ENOMEM, "qgemm_create: out of host memory");
@@ -830,6 +895,8 @@ size_t qgemm_workspace_bytes(const qgemm_plan *plan, int64_t B)
 {
     if (!plan || plan->magic != PLAN_MAGIC || B <= 0 || B > (1ll << 30))
         return 0;
+    if (plan->p.fmt == FMT_I8)
+        return (size_t)(ws_data_off(plan->p) + i8_part_bytes(plan, B) + i8_rows_bytes(plan->p, B));
     const int tier = choose_tier(plan, B);
     if (tier == QGEMM_TIER_GEMV)
         return 0;
@@ -867,6 +934,22 @@ static int check_run(const qgemm_plan *plan, int64_t B, const void *w, const voi
     return QGEMM_OK;
 }
 
+// The INT8 product of B > 0 rows of codes; `part` (part_bytes) holds the
+// partial tiles of a K split, or null.
+static int i8_product(const qgemm_plan *plan, const I8Args &a, uint8_t *part, int64_t part_bytes, hipStream_t st)
+{
+    hipError_t e;
+    if (i8_tier(plan, a.B) == QGEMM_TIER_SKINNY) {
+        e = launch_i8_small(a, plan->p.out, st);
+    } else {
+        I8TiCfg c = i8_tiled_cfg(a, part != nullptr);
+        if (c.part_bytes > part_bytes)
+            c = i8_tiled_cfg(a, false);
+        e = launch_i8_tiled(a, c, (int32_t *)part, plan->p.out, st);
+    }
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run: kernel launch");
+}
+
 // One call on arguments check_run accepted, with B > 0.  Scratch is two
 // regions: counter words at `cnt` (ws_data_off(p) bytes, zero between calls:
 // every call re-arms the ones it used) and partial tiles and the rounded
@@ -878,6 +961,26 @@ static int run_with(const qgemm_plan *plan, int64_t B, const void *w, const void
     const Problem &p = plan->p;
     if (!cnt)
         data_bytes = -1;
+    if (p.fmt == FMT_I8) {
+        const int64_t need = i8_rows_bytes(p, B), room = data_bytes - need;
+        if (room < 0)
+            return fail(QGEMM_ENOTSUP, "qgemm_run: QGEMM_INT8 quantises the rows into a workspace of "
+                                       "qgemm_workspace_bytes (qgemm_run_ws or qgemm_run_noalloc), or takes codes "
+                                       "(qgemm_run_codes)");
+        // partial tiles first: at the size they may have, or none at all
+        const int64_t pb = i8_part_bytes(plan, B) <= room ? i8_part_bytes(plan, B) : 0;
+        RowsArgs r = {};
+        r.x = x;
+        r.codes = (int8_t *)(data + pb);
+        r.ldc = i8_code_stride(p);
+        r.scales = (float *)(data + pb + round_up(B * r.ldc, 256));
+        r.B = B;
+        r.K = p.K;
+        const hipError_t e = launch_quantize_rows(p.act, r, st);
+        if (e != hipSuccess)
+            return hip_fail(e, "qgemm_run: kernel launch");
+        return i8_product(plan, i8_args(p, B, w, r.codes, r.ldc, r.scales, y), pb ? data : nullptr, pb, st);
+    }
     const KArgs a = make_args(p, B, w, x, y);
     hipError_t e;
     const int tier = choose_tier(plan, B);
@@ -1016,6 +1119,8 @@ static int grouped_tier(const qgemm_plan *plan, int64_t E, int64_t T)
     const Problem &p = plan->p;
     if (plan->forced_tier == QGEMM_TIER_GEMV)
         return 0;
+    if (p.fmt == FMT_I8)
+        return plan->forced_tier ? plan->forced_tier : T < 64 * E ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
     const int64_t xsz = p.act == QGEMM_F32 ? 4 : 2;
     const bool small_ok = p.math == QGEMM_MATH_BF16 && T * p.K * xsz < (1ll << 31) &&
                           E * moe_groups(p) <= 0x7FFFFFFFll && moe_groups_per_wg(p, E) >= 1;
@@ -1043,6 +1148,8 @@ int qgemm_run_grouped(const qgemm_plan *plan, int64_t E, int64_t T, const void *
         return fail(QGEMM_EINVAL, "qgemm_run_grouped: E=%lld outside 1..2^16", (long long)E);
     if (T < 0 || T > (1ll << 30))
         return fail(QGEMM_EINVAL, "qgemm_run_grouped: T=%lld outside 0..2^30", (long long)T);
+    if (p.fmt == FMT_I8)
+        return fail(QGEMM_ENOTSUP, "qgemm_run_grouped: QGEMM_INT8 takes codes (qgemm_run_grouped_codes)");
     const int tier = grouped_tier(plan, E, T);
     if (!tier)
         return fail(QGEMM_ENOTSUP, "qgemm_run_grouped: a plan forced to the GEMV tier, or to the small-batch "
@@ -1142,10 +1249,290 @@ int qgemm_dequantize(qgemm_format fmt, const void *w, float *w_out, int64_t N, i
     a.RT = (int)L.RT;
     a.scale_off = L.scale_off;
     a.meta_off = L.meta_off;
+    if (fmt == QGEMM_INT8 && L.RT * L.S * 64 > 0x7FFFFFFFll * 256)
+        return fail(QGEMM_EINVAL, "qgemm_dequantize: too large");
     hipError_t e0 = launch_dequant((int)fmt, a, w_out, (hipStream_t)stream);
     if (e0 != hipSuccess)
         return hip_fail(e0, "qgemm_dequantize: kernel launch");
     return QGEMM_OK;
+}
+
+// ------------------------------------------------ 8-bit rows and products
+
+// A pitch of codes: bytes from row to row.
+static bool bad_pitch(int64_t K, int64_t ldc) { return ldc < K || (ldc & 15) || ldc > (1ll << 21); }
+
+int qgemm_pack_device(qgemm_format fmt, int64_t N, int64_t K, const void *codes, const void *scales, void *out,
+                      size_t out_bytes, void *stream)
+{
+    Layout L;
+    if (!make_layout((int)fmt, N, K, &L))
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: bad format/shape (fmt=%d N=%lld K=%lld)", (int)fmt, (long long)N,
+                    (long long)K);
+    if (fmt != QGEMM_INT8)
+        return fail(QGEMM_ENOTSUP, "qgemm_pack_device: QGEMM_INT8 only");
+    if (N > (1ll << 30) || K > I8_MAX_K)
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: N above 2^30 or K above %lld", (long long)I8_MAX_K);
+    if (!codes || !scales || !out)
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: null pointer");
+    if (((uintptr_t)scales & 3u) || !aligned16(out))
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: misaligned pointer");
+    if (out_bytes < (size_t)L.total)
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: output buffer %zu bytes < %lld needed", out_bytes,
+                    (long long)L.total);
+    if (L.total / 16 > 0x7FFFFFFFll * 256)
+        return fail(QGEMM_EINVAL, "qgemm_pack_device: too large");
+    const hipError_t e = launch_i8_pack(L, (const int8_t *)codes, (const float *)scales, (uint8_t *)out,
+                                        (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_pack_device: kernel launch");
+}
+
+static int check_rows(const char *who, qgemm_dtype act, int64_t B, int64_t K, const void *x, const void *codes,
+                      int64_t ldc, const void *scales)
+{
+    if (act != QGEMM_F32 && act != QGEMM_BF16)
+        return fail(QGEMM_EINVAL, "%s: unknown dtype", who);
+    if (B < 0 || B > (1ll << 30) || K < 1 || K > (1ll << 20))
+        return fail(QGEMM_EINVAL, "%s: B=%lld outside 0..2^30 or K=%lld outside 1..2^20", who, (long long)B,
+                    (long long)K);
+    if (bad_pitch(K, ldc))
+        return fail(QGEMM_EINVAL, "%s: the pitch of the codes (%lld) is below K=%lld, above 2^21 or no multiple of 16",
+                    who, (long long)ldc, (long long)K);
+    if (B == 0)
+        return QGEMM_OK;
+    if (!x || !codes || !scales)
+        return fail(QGEMM_EINVAL, "%s: null pointer", who);
+    if (!aligned16(x) || !aligned16(codes) || ((uintptr_t)scales & 3u))
+        return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
+    return QGEMM_OK;
+}
+
+int qgemm_quantize_rows(qgemm_dtype act, int64_t B, int64_t K, const void *x, int8_t *codes, int64_t ldc,
+                        float *scales, void *stream)
+{
+    const int r = check_rows("qgemm_quantize_rows", act, B, K, x, codes, ldc, scales);
+    if (r != QGEMM_OK || B == 0)
+        return r;
+    RowsArgs a = {};
+    a.x = x;
+    a.codes = codes;
+    a.scales = scales;
+    a.B = B;
+    a.K = K;
+    a.ldc = ldc;
+    const hipError_t e = launch_quantize_rows((int)act, a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_quantize_rows: kernel launch");
+}
+
+static int check_codes(const char *who, const qgemm_plan *plan, int64_t B, const void *codes, int64_t ldc,
+                       const void *scales, const void *y)
+{
+    if (!plan || plan->magic != PLAN_MAGIC)
+        return fail(QGEMM_EINVAL, "%s: not a live plan", who);
+    const Problem &p = plan->p;
+    if (p.fmt != FMT_I8)
+        return fail(QGEMM_ENOTSUP, "%s: the plan's weights are not QGEMM_INT8", who);
+    if (B < 0 || B > (1ll << 30))
+        return fail(QGEMM_EINVAL, "%s: %lld rows outside 0..2^30", who, (long long)B);
+    if (bad_pitch(p.K, ldc))
+        return fail(QGEMM_EINVAL, "%s: the pitch of the codes (%lld) is below K=%lld, above 2^21 or no multiple of 16",
+                    who, (long long)ldc, (long long)p.K);
+    if (B == 0)
+        return QGEMM_OK;
+    if (!codes || !scales || !y)
+        return fail(QGEMM_EINVAL, "%s: null pointer", who);
+    if (!aligned16(codes) || !aligned16(y) || ((uintptr_t)scales & 3u))
+        return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
+    const int64_t ncols = p.epi == QGEMM_EPI_SWIGLU ? p.N / 2 : p.N;
+    if (B * ldc > (1ll << 31) - 1 || B * ncols > (1ll << 31) - 1)
+        return fail(QGEMM_EINVAL, "%s: codes or outputs above 2^31 elements", who);
+    return QGEMM_OK;
+}
+
+int qgemm_run_codes(const qgemm_plan *plan, int64_t B, const void *w, const int8_t *codes, int64_t ldc,
+                    const float *scales, void *y, void *workspace, size_t ws_bytes, void *stream)
+{
+    const int r = check_codes("qgemm_run_codes", plan, B, codes, ldc, scales, y);
+    if (r != QGEMM_OK || B == 0)
+        return r;
+    if (!w || !aligned16(w))
+        return fail(QGEMM_EINVAL, "qgemm_run_codes: w is null or not 16-byte aligned");
+    if (workspace && ((uintptr_t)workspace & 255u))
+        return fail(QGEMM_EINVAL, "qgemm_run_codes: workspace must be 256-byte aligned");
+    const int64_t off = ws_data_off(plan->p), room = workspace ? (int64_t)ws_bytes - off : -1;
+    return i8_product(plan, i8_args(plan->p, B, w, codes, ldc, scales, y),
+                      room > 0 ? (uint8_t *)workspace + off : nullptr, room, (hipStream_t)stream);
+}
+
+int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const void *const *w_table,
+                            const int32_t *offsets, const int8_t *codes, int64_t ldc, const float *scales, void *y,
+                            void *stream)
+{
+    if (E < 1 || E > (1 << 16))
+        return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: E=%lld outside 1..2^16", (long long)E);
+    const int r = check_codes("qgemm_run_grouped_codes", plan, T, codes, ldc, scales, y);
+    if (r != QGEMM_OK || T == 0)
+        return r;
+    if (!w_table || !offsets)
+        return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: null pointer");
+    if (((uintptr_t)w_table & 7u) || ((uintptr_t)offsets & 3u))
+        return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: misaligned pointer");
+    I8Groups g;
+    g.wtab = (const uint8_t *const *)w_table;
+    g.off = offsets;
+    g.E = (int)E;
+    g.status = status_word(current_device());
+    if (!g.status)
+        return fail(QGEMM_EHIP, "qgemm_run_grouped_codes: no device status word");
+    const I8Args a = i8_args(plan->p, T, nullptr, codes, ldc, scales, y);
+    const bool small = grouped_tier(plan, E, T) == QGEMM_TIER_SKINNY;
+    // row groups of 16 channels at least, or tiles of 128 x 128 at least
+    if (small ? E * ((int64_t)a.RT + 1) > 0x7FFFFFFFll : (T / 64 + (E < T ? E : T)) * ((int64_t)a.RT / 4 + 1) > 0x7FFFFFFFll)
+        return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: grid too large");
+    const hipError_t e = small ? launch_i8_small_grouped(a, g, plan->p.out, (hipStream_t)stream)
+                               : launch_i8_tiled_grouped(a, g, plan->p.out, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run_grouped_codes: kernel launch");
+}
+
+// ------------------------------------------------ rows sorted by expert
+
+int qgemm_route(int64_t E, int64_t T, int64_t topk, const int32_t *ids, int32_t *offsets, int32_t *pos, void *stream)
+{
+    if (E < 1 || E > (1 << 16))
+        return fail(QGEMM_EINVAL, "qgemm_route: E=%lld outside 1..2^16", (long long)E);
+    if (E > ROUTE_MAX_E)
+        return fail(QGEMM_ENOTSUP, "qgemm_route: the counters of E=%lld experts do not fit in LDS (E <= %d)",
+                    (long long)E, ROUTE_MAX_E);
+    if (T < 0 || T > (1ll << 30) || topk < 1 || topk > QGEMM_MAX_TOPK || T * topk > (1ll << 30))
+        return fail(QGEMM_EINVAL, "qgemm_route: T=%lld, topk=%lld outside 0..2^30, 1..%d, or more than 2^30 choices",
+                    (long long)T, (long long)topk, QGEMM_MAX_TOPK);
+    if (!offsets || (T > 0 && (!ids || !pos)))
+        return fail(QGEMM_EINVAL, "qgemm_route: null pointer");
+    if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)pos) & 3u)
+        return fail(QGEMM_EINVAL, "qgemm_route: misaligned pointer");
+    RouteArgs a = {ids, offsets, pos, (int)(T * topk), (int)E};
+    const hipError_t e = launch_route(a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_route: kernel launch");
+}
+
+static int check_moves(const char *who, qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R)
+{
+    if (dt != QGEMM_F32 && dt != QGEMM_BF16)
+        return fail(QGEMM_EINVAL, "%s: unknown dtype", who);
+    if (T < 0 || T > (1ll << 30) || topk < 1 || topk > QGEMM_MAX_TOPK || T * topk > (1ll << 30))
+        return fail(QGEMM_EINVAL, "%s: T=%lld, topk=%lld outside 0..2^30, 1..%d, or more than 2^30 choices", who,
+                    (long long)T, (long long)topk, QGEMM_MAX_TOPK);
+    if (H < 1 || H > (1ll << 20) || R < 0 || R > (1ll << 30))
+        return fail(QGEMM_EINVAL, "%s: H=%lld outside 1..2^20 or R=%lld outside 0..2^30", who, (long long)H,
+                    (long long)R);
+    return QGEMM_OK;
+}
+
+static MoveArgs move_args(int64_t T, int64_t topk, int64_t H, int64_t R, const int32_t *pos)
+{
+    MoveArgs a = {};
+    a.pos = pos;
+    a.T = T;
+    a.H = H;
+    a.R = R;
+    a.topk = (int)topk;
+    a.status = status_word(current_device());
+    return a;
+}
+
+int qgemm_dispatch(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *x, const int32_t *pos,
+                   void *xs, void *stream)
+{
+    const int r = check_moves("qgemm_dispatch", dt, T, topk, H, R);
+    if (r != QGEMM_OK || T == 0)
+        return r;
+    if (!x || !pos || (R > 0 && !xs))
+        return fail(QGEMM_EINVAL, "qgemm_dispatch: null pointer");
+    if (!aligned16(x) || !aligned16(xs) || ((uintptr_t)pos & 3u))
+        return fail(QGEMM_EINVAL, "qgemm_dispatch: misaligned pointer");
+    MoveArgs a = move_args(T, topk, H, R, pos);
+    if (!a.status)
+        return fail(QGEMM_EHIP, "qgemm_dispatch: no device status word");
+    a.src = x;
+    a.dst = xs;
+    const hipError_t e = launch_dispatch((int)dt, a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_dispatch: kernel launch");
+}
+
+int qgemm_dispatch_codes(qgemm_dtype act, int64_t T, int64_t topk, int64_t K, int64_t R, const void *x,
+                         const int32_t *pos, int8_t *codes, int64_t ldc, float *scales, void *stream)
+{
+    int r = check_moves("qgemm_dispatch_codes", act, T, topk, K, R);
+    if (r != QGEMM_OK)
+        return r;
+    if (R == 0 && T > 0) {  // nothing can be named
+        if (!x || !pos)
+            return fail(QGEMM_EINVAL, "qgemm_dispatch_codes: null pointer");
+        return QGEMM_OK;
+    }
+    r = check_rows("qgemm_dispatch_codes", act, T, K, x, codes, ldc, scales);
+    if (r != QGEMM_OK || T == 0)
+        return r;
+    if (!pos || ((uintptr_t)pos & 3u))
+        return fail(QGEMM_EINVAL, "qgemm_dispatch_codes: pos is null or misaligned");
+    RowsArgs a = {};
+    a.x = x;
+    a.codes = codes;
+    a.scales = scales;
+    a.pos = pos;
+    a.B = T;
+    a.K = K;
+    a.ldc = ldc;
+    a.R = R;
+    a.topk = (int)topk;
+    a.status = status_word(current_device());
+    if (!a.status)
+        return fail(QGEMM_EHIP, "qgemm_dispatch_codes: no device status word");
+    const hipError_t e = launch_quantize_rows((int)act, a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_dispatch_codes: kernel launch");
+}
+
+int qgemm_combine(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *ys, const int32_t *pos,
+                  const float *weights, void *y, void *stream)
+{
+    const int r = check_moves("qgemm_combine", dt, T, topk, H, R);
+    if (r != QGEMM_OK || T == 0)
+        return r;
+    if ((R > 0 && !ys) || !pos || !y)
+        return fail(QGEMM_EINVAL, "qgemm_combine: null pointer");
+    if (!aligned16(ys) || !aligned16(y) || (((uintptr_t)pos | (uintptr_t)weights) & 3u))
+        return fail(QGEMM_EINVAL, "qgemm_combine: misaligned pointer");
+    MoveArgs a = move_args(T, topk, H, R, pos);
+    if (!a.status)
+        return fail(QGEMM_EHIP, "qgemm_combine: no device status word");
+    a.src = ys;
+    a.weights = weights;
+    a.dst = y;
+    const hipError_t e = launch_combine((int)dt, a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_combine: kernel launch");
+}
+
+int qgemm_combine_grad(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64_t R, const void *dy, const void *ys,
+                       const int32_t *pos, const float *weights, void *dys, float *dw, void *stream)
+{
+    const int r = check_moves("qgemm_combine_grad", dt, T, topk, H, R);
+    if (r != QGEMM_OK || T == 0)
+        return r;
+    if (!dy || (R > 0 && (!ys || !dys)) || !pos || !weights || !dw)
+        return fail(QGEMM_EINVAL, "qgemm_combine_grad: null pointer");
+    if (!aligned16(dy) || !aligned16(ys) || !aligned16(dys) ||
+        (((uintptr_t)pos | (uintptr_t)weights | (uintptr_t)dw) & 3u))
+        return fail(QGEMM_EINVAL, "qgemm_combine_grad: misaligned pointer");
+    MoveArgs a = move_args(T, topk, H, R, pos);
+    if (!a.status)
+        return fail(QGEMM_EHIP, "qgemm_combine_grad: no device status word");
+    a.src = dy;
+    a.src2 = ys;
+    a.weights = weights;
+    a.dst = dys;
+    a.dw = dw;
+    const hipError_t e = launch_combine_grad((int)dt, a, (hipStream_t)stream);
+    return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_combine_grad: kernel launch");
 }
 
 }  // extern "C"

@@ -53,8 +53,31 @@ __global__ __launch_bounds__(256) void dequant_kernel(KArgs a, float *out)
     *(f32x4 *)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// INT8: one thread per 16-byte chunk of the codes, t * c rounded once.
+__global__ __launch_bounds__(256) void dequant_i8_kernel(KArgs a, float *out)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.RT * a.S * 64)
+        return;
+    const int64_t slab = i >> 6;
+    const int lane = (int)(i & 63);
+    const int64_t n = slab / a.S * 16 + (lane & 15);
+    const int k0 = (int)(slab % a.S) * 64 + (lane >> 4) * 16;
+    if (n >= a.N || k0 >= a.K)
+        return;
+    const float t = ((const float *)(a.w + a.scale_off))[n];
+    const int8_t *c = (const int8_t *)a.w + i * 16;
+    for (int j = 0; j < 16 && k0 + j < a.K; j++)
+        out[n * a.K + k0 + j] = (float)c[j] * t;
+}
+
 hipError_t launch_dequant(int fmt, const KArgs &a, float *out, hipStream_t st)
 {
+    if (fmt == FMT_I8) {
+        const int64_t chunks = (int64_t)a.RT * a.S * 64;
+        hipLaunchKernelGGL(dequant_i8_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st, a, out);
+        return hipGetLastError();
+    }
     const int64_t threads = (int64_t)a.N * (a.K / 8);
     const dim3 grid((unsigned)((threads + 255) / 256));
     switch (fmt) {

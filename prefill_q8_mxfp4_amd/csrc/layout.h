@@ -6,7 +6,10 @@
 // each 32-wide unit of the slab (row L % 16, k-group L / 16).  Scales follow,
 // one contiguous record of the 16 rows per (row tile, slab) in the codes'
 // order, so the scales of a slab are one 64-byte (128-byte for NVFP4) piece
-// of a cache line; NVFP4 adds a 256-byte tensor-scale record.
+// of a cache line; NVFP4 adds a 256-byte tensor-scale record.  INT8 slabs
+// hold 64 weights along K whose chunk L is lane L's operand of one 16x16x64
+// int8 MFMA (row L % 16, k = 16 * (L / 16) + 0..15); K is padded to two slabs
+// and one fp32 scale a row follows the codes.
 #pragma once
 #include <stdint.h>
 
@@ -14,7 +17,7 @@
 
 namespace qg {
 
-enum { FMT_Q8 = 0, FMT_MX = 1, FMT_NV = 2, FMT_FP8 = 3 };
+enum { FMT_Q8 = 0, FMT_MX = 1, FMT_NV = 2, FMT_FP8 = 3, FMT_I8 = 4 };
 
 struct Layout {
     int64_t N, K;
@@ -50,16 +53,20 @@ __host__ __device__ static inline int64_t scale_offset(int64_t scale_off, int64_
 
 static inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-static inline int64_t block_of(int fmt) { return fmt == FMT_NV ? 16 : 32; }
+// K has to be a multiple of this (INT8 has no blocks: any K).
+static inline int64_t block_of(int fmt) { return fmt == FMT_I8 ? 1 : fmt == FMT_NV ? 16 : 32; }
 
 // Weights per slab along K: 64 for the byte formats, 128 for the FP4 ones.
-__host__ __device__ constexpr int slab_k(int fmt) { return fmt == FMT_Q8 || fmt == FMT_FP8 ? 64 : 128; }
+__host__ __device__ constexpr int slab_k(int fmt)
+{
+    return fmt == FMT_Q8 || fmt == FMT_FP8 || fmt == FMT_I8 ? 64 : 128;
+}
 
 constexpr int FP8_BLOCK = 128;  // weights per FP8 block scale along K
 
 static inline bool make_layout(int fmt, int64_t N, int64_t K, Layout *L)
 {
-    if (fmt < FMT_Q8 || fmt > FMT_FP8 || N <= 0 || K <= 0)
+    if (fmt < FMT_Q8 || fmt > FMT_I8 || N <= 0 || K <= 0)
         return false;
     if (K % block_of(fmt))
         return false;
@@ -68,11 +75,16 @@ static inline bool make_layout(int fmt, int64_t N, int64_t K, Layout *L)
     L->blk = block_of(fmt);
     L->KS = slab_k(fmt);
     L->Np = round_up(N, 16);
-    L->Kp = round_up(K, L->KS);
+    L->Kp = round_up(K, fmt == FMT_I8 ? 2 * L->KS : L->KS);
     L->S = L->Kp / L->KS;
     L->RT = L->Np / 16;
     int64_t codes = L->RT * L->S * 1024;
     L->scale_off = round_up(codes, QGEMM_ALIGN);
+    if (fmt == FMT_I8) {
+        L->meta_off = -1;
+        L->total = round_up(L->scale_off + L->Np * 4, QGEMM_ALIGN);
+        return true;
+    }
     int64_t end = L->scale_off + L->RT * L->S * scale_record_bytes(fmt);
     if (fmt == FMT_NV) {
         L->meta_off = round_up(end, QGEMM_ALIGN);
