@@ -152,7 +152,7 @@ typedef enum qgemm_tier {
  *      FP8  : byte 8u + j is the E4M3 code, as for Q8_0;
  *      FP4  : byte 4u + j holds the codes of k = ... + 2j (low nibble) and
  *             ... + 2j + 1 (high nibble), u = 0..3.
- *    INT8 differs: KS = 64, K padded to a multiple of 128, and chunk L holds
+ *    INT8 differs: KS = 64, K padded to a multiple of 256, and chunk L holds
  *    the sixteen codes k = s*KS + 16g + 0..15 of row r in order.
  * 2. Scales: at a QGEMM_ALIGN-rounded offset, one record per slab, in the
  *    codes' order: record (rt, s) is at ((rt * S) + s) * 16 * E and its bytes

@@ -249,6 +249,7 @@ class Plan:
         _check(lib().qgemm_create(ctypes.byref(h), FORMATS[fmt], DTYPES[act], DTYPES[out],
                                   EPILOGUES[epilogue], MATHS[math], N, K, flags))
         self._h = h
+        self.weight_bytes = weight_bytes(fmt, N, K)
 
     @property
     def out_cols(self) -> int:
@@ -309,8 +310,10 @@ class Plan:
             raise TypeError("dtype mismatch: x %s, w %s, y %s" % (x.dtype, w.dtype, y.dtype))
         if x.numel() < B * self.K or y.numel() < B * self.out_cols:
             raise ValueError("x or y too small for B")
-        if w.numel() < weight_bytes(self.fmt, self.N, self.K):
+        if w.numel() < self.weight_bytes:
             raise ValueError("packed weight buffer too small")
+        if self.fmt == "int8":
+            return self._run_int8(x, w, y, stream, B, workspace)
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         init_device(x.device)
@@ -337,7 +340,7 @@ class Plan:
             raise TypeError("dtype mismatch: x %s, w %s, y %s" % (x.dtype, w.dtype, y.dtype))
         if x.numel() < B * self.K or y.numel() < B * self.out_cols:
             raise ValueError("x or y too small for B")
-        if w.numel() < weight_bytes(self.fmt, self.N, self.K):
+        if w.numel() < self.weight_bytes:
             raise ValueError("packed weight buffer too small")
         init_device(x.device)
         _check(lib().qgemm_run_noalloc(self._h, B, _dev_ptr(w, "w"), _dev_ptr(x, "x"),
@@ -379,16 +382,44 @@ class Plan:
             raise TypeError("dtype mismatch: w %s, y %s" % (w.dtype, y.dtype))
         if y.numel() < B * self.out_cols:
             raise ValueError("y too small for B")
-        if w.numel() < weight_bytes(self.fmt, self.N, self.K):
+        if w.numel() < self.weight_bytes:
             raise ValueError("packed weight buffer too small")
-        with _device_of(codes, scales, w, y) as dev:
-            st = torch.cuda.current_stream(codes.device) if stream is None else stream
-            if isinstance(workspace, str):
-                workspace = self._workspace(B, codes.device, st) if B > 0 else None
-            wsp, wsn = (0, 0) if workspace is None else (_dev_ptr(workspace, "workspace"), workspace.numel())
-            _check(lib().qgemm_run_codes(self._h, B, _dev_ptr(w, "w"), codes.data_ptr(), ldc,
-                                         _dev_ptr(scales, "scales"), _dev_ptr(y, "y"), wsp, wsn, st.cuda_stream))
+        dev = _gpu(codes)
+        wsp, wsn = self._workspace_of(workspace, B, dev, stream, codes=True)
+        _call(lib().qgemm_run_codes, dev, stream, self._h, B, _addr(w, "w", dev), codes.data_ptr(), ldc,
+              _addr(scales, "scales", dev), _addr(y, "y", dev), wsp, wsn)
         return y
+
+    def _run_int8(self, x, w, y, stream, B, workspace):
+        """run() of int8 weights: the rows are quantised into the workspace."""
+        dev = _gpu(x)
+        wsp, wsn = self._workspace_of(workspace, B, dev, stream)
+        _call(lib().qgemm_run_ws, dev, stream, self._h, B, _addr(w, "w", dev), _addr(x, "x", dev), _addr(y, "y", dev),
+              wsp, wsn)
+        return y
+
+    def _workspace_of(self, workspace, B, dev, stream, codes=False):
+        """(address, bytes) of an int8 call's workspace: the caller's, none, or
+        ("auto") the plan's.  The plan's is asked for again only when the width,
+        the device or the stream is not the last call's."""
+        import torch
+
+        if workspace is None:
+            return 0, 0
+        if not isinstance(workspace, str):
+            return _addr(workspace, "workspace", dev), workspace.numel()
+        if B == 0:
+            return 0, 0
+        if codes and self.tier(B) == "skinny":
+            return 0, 0                     # nothing to split or to quantise
+        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        key = (B, dev, raw)
+        last = self.__dict__.get("_ws_last")
+        if last is None or last[0] != key or torch.cuda.is_current_stream_capturing():
+            st = torch.cuda.current_stream(dev) if stream is None else stream
+            ws = self._workspace(B, torch.device("cuda", dev), st)
+            last = self._ws_last = (key, ws.data_ptr(), ws.numel())
+        return last[1], last[2]
 
     def run_grouped_codes(self, codes, scales, w_table, offsets, y, stream=None):
         """qgemm_run_grouped_codes: routed experts on rows of codes sorted by
@@ -405,10 +436,9 @@ class Plan:
             raise TypeError("w_table must be int64 [E], offsets int32 [E + 1]")
         if y.numel() < T * self.out_cols:
             raise ValueError("y too small")
-        with _device_of(codes, scales, w_table, offsets, y) as dev:
-            _check(lib().qgemm_run_grouped_codes(
-                self._h, E, T, _dev_ptr(w_table, "w_table"), _dev_ptr(offsets, "offsets"), codes.data_ptr(), ldc,
-                _dev_ptr(scales, "scales"), _dev_ptr(y, "y"), _raw_stream(stream, dev)))
+        dev = _gpu(codes)
+        _call(lib().qgemm_run_grouped_codes, dev, stream, self._h, E, T, _addr(w_table, "w_table", dev),
+              _addr(offsets, "offsets", dev), codes.data_ptr(), ldc, _addr(scales, "scales", dev), _addr(y, "y", dev))
         return y
 
     def close(self):
@@ -423,38 +453,56 @@ class Plan:
             pass
 
 
-class _device_of:
-    """The one device of the tensors, made the current one inside the block
-    (kernels, the status word and streams belong to it)."""
+class _on_device:
+    """The tensors' device as the current one inside the block (kernels, the
+    status word and streams belong to it); only entered when it is another."""
 
     __slots__ = ("index", "before")
 
-    def __init__(self, *tensors):
-        d = tensors[0].device
-        for t in tensors:
-            if t.device != d or d.type != "cuda":
-                raise ValueError("tensors must be on one CUDA (HIP) device")
-        self.index = d.index
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
         import torch
 
         self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return self.index
+        torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
         import torch
 
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+        torch.cuda.set_device(self.before)
 
 
-def _raw_stream(stream, index):
+def _gpu(t):
+    """Index of a tensor's GPU."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA (HIP) device")
+    return dev
+
+
+def _addr(t, name, dev):
+    """Address of a contiguous tensor on GPU dev."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the CUDA (HIP) device of the others" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _call(f, dev, stream, *args):
+    """One call of an entry point whose last argument is the stream, on GPU
+    dev.  A call costs a few microseconds of host time, which bounds the small
+    ones: the raw stream is asked for (0.1 us) rather than a Stream object (2 us)."""
     import torch
 
-    return torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() != dev:
+        with _on_device(dev):
+            return _call(f, dev, stream, *args)
+    status = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status != OK:
+        _check(status)
 
 
 def code_stride(K: int) -> int:
@@ -482,6 +530,12 @@ def _codes_pitch(codes, scales, K):
     return B, ldc
 
 
+def _codes_addr(codes, dev):
+    if codes.get_device() != dev:
+        raise ValueError("codes must be on the CUDA (HIP) device of the others")
+    return codes.data_ptr()
+
+
 def _rows_dtype(t, name):
     import torch
 
@@ -507,9 +561,9 @@ def pack_int8(codes, scales, out=None, stream=None):
         out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
     if out.dtype != torch.uint8 or out.numel() < nbytes:
         raise ValueError("out must be uint8, at least %d bytes" % nbytes)
-    with _device_of(codes, scales, out) as dev:
-        _check(lib().qgemm_pack_device(FORMATS["int8"], N, K, _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"),
-                                       _dev_ptr(out, "out"), out.numel(), _raw_stream(stream, dev)))
+    dev = _gpu(codes)
+    _call(lib().qgemm_pack_device, dev, stream, FORMATS["int8"], N, K, _addr(codes, "codes", dev),
+          _addr(scales, "scales", dev), _addr(out, "out", dev), out.numel())
     return out
 
 
@@ -536,9 +590,9 @@ def quantize_rows(x, codes=None, scales=None, stream=None):
     rows, ldc = _codes_pitch(codes, scales, K)
     if rows != B:
         raise ValueError("codes must have x's rows")
-    with _device_of(x, codes, scales) as dev:
-        _check(lib().qgemm_quantize_rows(dt, B, K, _dev_ptr(x, "x"), codes.data_ptr(), ldc,
-                                         _dev_ptr(scales, "scales"), _raw_stream(stream, dev)))
+    dev = _gpu(x)
+    _call(lib().qgemm_quantize_rows, dev, stream, dt, B, K, _addr(x, "x", dev), _codes_addr(codes, dev), ldc,
+          _addr(scales, "scales", dev))
     return codes, scales
 
 
@@ -559,9 +613,9 @@ def route(ids, E: int, offsets=None, pos=None, stream=None):
         raise TypeError("offsets and pos must be int32")
     if offsets.numel() != E + 1 or pos.shape != ids.shape:
         raise ValueError("offsets must be [E + 1], pos as ids")
-    with _device_of(ids, offsets, pos) as dev:
-        _check(lib().qgemm_route(E, ids.shape[0], ids.shape[1], _dev_ptr(ids, "ids"), _dev_ptr(offsets, "offsets"),
-                                 _dev_ptr(pos, "pos"), _raw_stream(stream, dev)))
+    dev = _gpu(ids)
+    _call(lib().qgemm_route, dev, stream, E, ids.shape[0], ids.shape[1], _addr(ids, "ids", dev),
+          _addr(offsets, "offsets", dev), _addr(pos, "pos", dev))
     return offsets, pos
 
 
@@ -592,9 +646,9 @@ def dispatch(x, pos, xs, stream=None):
     dt = _rows_dtype(x, "x")
     _check_rows(xs, x, "xs")
     _check_pos(pos, x.shape[0])
-    with _device_of(x, pos, xs) as dev:
-        _check(lib().qgemm_dispatch(dt, x.shape[0], pos.shape[1], x.shape[1], xs.shape[0], _dev_ptr(x, "x"),
-                                    _dev_ptr(pos, "pos"), _dev_ptr(xs, "xs"), _raw_stream(stream, dev)))
+    dev = _gpu(x)
+    _call(lib().qgemm_dispatch, dev, stream, dt, x.shape[0], pos.shape[1], x.shape[1], xs.shape[0],
+          _addr(x, "x", dev), _addr(pos, "pos", dev), _addr(xs, "xs", dev))
     return xs
 
 
@@ -606,10 +660,9 @@ def dispatch_codes(x, pos, codes, scales, stream=None):
         raise ValueError("x must be [T][K]")
     _check_pos(pos, x.shape[0])
     R, ldc = _codes_pitch(codes, scales, x.shape[1])
-    with _device_of(x, pos, codes, scales) as dev:
-        _check(lib().qgemm_dispatch_codes(dt, x.shape[0], pos.shape[1], x.shape[1], R, _dev_ptr(x, "x"),
-                                          _dev_ptr(pos, "pos"), codes.data_ptr(), ldc, _dev_ptr(scales, "scales"),
-                                          _raw_stream(stream, dev)))
+    dev = _gpu(x)
+    _call(lib().qgemm_dispatch_codes, dev, stream, dt, x.shape[0], pos.shape[1], x.shape[1], R, _addr(x, "x", dev),
+          _addr(pos, "pos", dev), _codes_addr(codes, dev), ldc, _addr(scales, "scales", dev))
     return codes, scales
 
 
@@ -619,14 +672,12 @@ def combine(ys, pos, weights, y, stream=None):
     dt = _rows_dtype(ys, "ys")
     _check_rows(y, ys, "y")
     _check_pos(pos, y.shape[0])
-    tensors = (ys, pos, y)
     if weights is not None:
         _check_weights(weights, pos)
-        tensors += (weights,)
-    with _device_of(*tensors) as dev:
-        _check(lib().qgemm_combine(dt, y.shape[0], pos.shape[1], y.shape[1], ys.shape[0], _dev_ptr(ys, "ys"),
-                                   _dev_ptr(pos, "pos"), None if weights is None else _dev_ptr(weights, "weights"),
-                                   _dev_ptr(y, "y"), _raw_stream(stream, dev)))
+    dev = _gpu(ys)
+    wp = None if weights is None else _addr(weights, "weights", dev)
+    _call(lib().qgemm_combine, dev, stream, dt, y.shape[0], pos.shape[1], y.shape[1], ys.shape[0],
+          _addr(ys, "ys", dev), _addr(pos, "pos", dev), wp, _addr(y, "y", dev))
     return y
 
 
@@ -647,10 +698,10 @@ def combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
     _check_weights(dw, pos, "dw")
     if dys.shape[0] != ys.shape[0]:
         raise ValueError("dys must have ys's rows")
-    with _device_of(dy, ys, pos, weights, dys, dw) as dev:
-        _check(lib().qgemm_combine_grad(dt, dy.shape[0], pos.shape[1], dy.shape[1], ys.shape[0], _dev_ptr(dy, "dy"),
-                                        _dev_ptr(ys, "ys"), _dev_ptr(pos, "pos"), _dev_ptr(weights, "weights"),
-                                        _dev_ptr(dys, "dys"), _dev_ptr(dw, "dw"), _raw_stream(stream, dev)))
+    dev = _gpu(dy)
+    _call(lib().qgemm_combine_grad, dev, stream, dt, dy.shape[0], pos.shape[1], dy.shape[1], ys.shape[0],
+          _addr(dy, "dy", dev), _addr(ys, "ys", dev), _addr(pos, "pos", dev), _addr(weights, "weights", dev),
+          _addr(dys, "dys", dev), _addr(dw, "dw", dev))
     return dys, dw
 
 

@@ -1,32 +1,38 @@
 // 8-bit products with many rows: BM batch rows x BN channels a workgroup, both
 // operands staged through LDS by gfx950's direct loads, int32 accumulators.
 //
-// LDS holds matrix-core operands as they are fed: a 1 KB chunk is 16 channels
-// (or 16 rows) x 64 k, lane L's 16 bytes at 16 L.  A packed weight slab is
-// such a chunk already; a row group's chunk is gathered by the load itself
-// (lane L: row L % 16, k group L / 16), so every LDS access is a wave-wide
-// contiguous KB and no shuffle, decode or register staging is left.  A step is
-// 128 k (two chunks of each tile), two steps in LDS: the next one is loaded
-// while the current one is multiplied.
+// A step is 64 k.  A packed weight slab is 1 KB in the order in which the lanes
+// of a wave take it, so its load and its read are a contiguous KB each.  Rows of
+// codes are loaded 128 k at a time, whole cache lines (64-byte halves of them,
+// one a step, cost each line twice: 400 against 330 us at 2048 x 34816 x 5120):
+// a KB holds 8 rows x 128 k, with the eight 16-byte pieces of row r in the order
+// p ^ swizzle(r), so that the 16 lanes that read one k group of 16 rows together
+// find 16 different bank groups.  Nothing is decoded, shuffled or staged in
+// registers on the way.
+//
+// Four steps of weights and two double steps of codes are in LDS.  While a step
+// is multiplied, the next one's operands are read into registers and the loads
+// of the ones after it are in flight: a step's matrix time is far below the
+// latency of a load.  One barrier a step: it says that the next step has landed
+// (each wave waits for its own loads of it, and leaves the later ones in flight)
+// and that the present one is in every wave's registers, so that its place can
+// be loaded into again.  The same loads are issued in every fourth step, those
+// past the last step from an empty resource, so the counts waited for are exact.
 #include "int8.h"
 
 namespace qg {
-
-constexpr int I8_STEP = 128;  // k a step
 
 template <int WM_, int WN_, int TM_, int TN_>
 struct TiShape {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // waves, and 16-wide tiles a wave
     static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
-    static constexpr int XC = BM / 16 * 2, WC = BN / 16 * 2;  // chunks a step
-    static constexpr int XPW = XC / NW, WPW = WC / NW;        // of them a wave loads
-    static constexpr int STAGE = (XC + WC) * 1024;
-    static_assert(XC % NW == 0 && WC % NW == 0, "whole chunks a wave");
+    static constexpr int XC = BM / 8, WC = BN / 16;     // KBs of a double step of codes, of a step of weights
+    static constexpr int XPW = XC / NW, WPW = WC / NW;  // of them a wave loads
+    static constexpr int XST = XC * 1024, WST = WC * 1024;
+    static_assert(XC % NW == 0 && WC % NW == 0, "whole KBs a wave");
 };
-using TiBig = TiShape<2, 4, 8, 4>;    // 256 x 256, 8 waves of 128 x 64
-using TiMid = TiShape<2, 2, 4, 4>;    // 128 x 128, 4 waves of 64 x 64
-
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
+using TiBig = TiShape<2, 4, 8, 4>;  // 256 x 256, 8 waves of 128 x 64
+using TiMid = TiShape<2, 2, 4, 4>;  // 128 x 128, 4 waves of 64 x 64
 
 __device__ __forceinline__ void load_chunk(__amdgpu_buffer_rsrc_t r, uint8_t *lds, int voff, int soff)
 {
@@ -81,76 +87,141 @@ __device__ __forceinline__ void ti_store(const I8Args &a, const uint8_t *w, int6
     }
 }
 
-// One tile: rows row0 .. row0+rows-1 (at most BM), weight tile nt, steps k0 .. k1-1.
+// Waits until at most N of this wave's loads are in flight and its LDS reads are
+// done, then for the other waves.  Nothing moves across it.
+template <int N>
+__device__ __forceinline__ void step_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The order of a step's instructions: its loads (as many as wanted), then a read
+// every other matrix instruction, so that neither waits for the other.
+template <int LOADS, int READS, int MFMAS>
+__device__ __forceinline__ void ti_interleave()
+{
+#pragma unroll
+    for (int i = 0; i < LOADS; i++) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a load
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction
+    }
+    constexpr int PER = (MFMAS - LOADS) / READS > 0 ? (MFMAS - LOADS) / READS : 1;
+#pragma unroll
+    for (int i = 0; i < READS; i++) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// LDS of a workgroup.  Every buffer is an array of its own in the kernels: the
+// compiler tells the loads into one from the reads of another by the array.
+struct TiLds {
+    uint8_t *x[2], *w[4];
+};
+#define TI_LDS(S, L)                                                                      \
+    __shared__ __attribute__((aligned(1024))) uint8_t ldx0[S::XST], ldx1[S::XST];         \
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw0[S::WST], ldw1[S::WST];         \
+    __shared__ __attribute__((aligned(1024))) uint8_t ldw2[S::WST], ldw3[S::WST];         \
+    const TiLds L = {{ldx0, ldx1}, {ldw0, ldw1, ldw2, ldw3}}
+
+__device__ __forceinline__ int x_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// One tile: rows row0 .. row0+rows-1 (at most BM), weight tile nt, steps k0 .. k1-1
+// (a multiple of 4).
 template <typename S, bool DUAL>
 __device__ __forceinline__ void ti_tile_sums(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt, int k0,
-                                             int k1, uint8_t *st0, uint8_t *st1, i32x4 (&acc)[S::TM][S::TN])
+                                             int k1, const TiLds &lds, i32x4 (&acc)[S::TM][S::TN])
 {
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wid / S::WN, wn = wid % S::WN;
     const int64_t tile_bytes = (int64_t)a.S << 10;
 
-    // what this wave loads: row groups and weight tiles, both chunks of each
-    const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.codes + row0 * a.ldc, (int64_t)rows * a.ldc);
-    int xo[S::XPW / 2];
+    // what this wave loads: KBs of codes (rows past the last are copies of it)
+    // and weight tiles
+    const uint8_t *xbase = (const uint8_t *)a.codes + row0 * a.ldc;
+    const int64_t xbytes = (int64_t)rows * a.ldc;
+    int xo[S::XPW];
 #pragma unroll
-    for (int c = 0; c < S::XPW / 2; c++) {
-        const int b = min((wid * (S::XPW / 2) + c) * 16 + (lane & 15), rows - 1);
-        xo[c] = b * a.ldc + (lane >> 4) * 16;
+    for (int c = 0; c < S::XPW; c++) {
+        const int r = (wid * S::XPW + c) * 8 + (lane >> 3);
+        xo[c] = min(r, rows - 1) * a.ldc + (((lane & 7) ^ x_swizzle(r)) << 4);
     }
-    __amdgpu_buffer_rsrc_t wr[S::WPW / 2];
+    const uint8_t *wbase[S::WPW];
 #pragma unroll
-    for (int c = 0; c < S::WPW / 2; c++)
-        wr[c] = make_rsrc(w + ti_tile<S, DUAL>(a, nt, wid * (S::WPW / 2) + c) * tile_bytes, tile_bytes);
+    for (int c = 0; c < S::WPW; c++)
+        wbase[c] = w + ti_tile<S, DUAL>(a, nt, wid * S::WPW + c) * tile_bytes;
 
-    auto load = [&](int kt, uint8_t *st) {
-        uint8_t *xl = st + wid * S::XPW * 1024, *wl = st + (S::XC + wid * S::WPW) * 1024;
+    auto load_x = [&](int kt, uint8_t *to) {  // the double step kt, kt + 1
+        const bool live = kt < k1;
+        const __amdgpu_buffer_rsrc_t xr = make_rsrc(xbase, live ? xbytes : 0);
 #pragma unroll
         for (int c = 0; c < S::XPW; c++)
-            load_chunk(xr, xl + c * 1024, xo[c / 2] + (c & 1) * 64, kt * I8_STEP);
+            load_chunk(xr, to + (wid * S::XPW + c) * 1024, xo[c], live ? kt << 6 : 0);
+    };
+    auto load_w = [&](int kt, uint8_t *to) {
+        const bool live = kt < k1;
 #pragma unroll
         for (int c = 0; c < S::WPW; c++)
-            load_chunk(wr[c / 2], wl + c * 1024, lane * 16, (kt * 2 + (c & 1)) << 10);
+            load_chunk(make_rsrc(wbase[c], live ? tile_bytes : 0), to + (wid * S::WPW + c) * 1024, lane * 16,
+                       live ? kt << 10 : 0);
     };
-    auto compute = [&](const uint8_t *st) {
-        const uint8_t *xl = st + wm * S::TM * 2048 + lane * 16;
-        const uint8_t *wl = st + S::XC * 1024 + wn * S::TN * 2048 + lane * 16;
+    i32x4 xf[2][S::TM], wf[2][S::TN];
+    // row r = lane % 16 of a group of 16 and its k group, in the even step; the
+    // odd step's piece is 4 further on, which the swizzle leaves a flip of one bit
+    const int r16 = lane & 15;
+    const int xl = wm * S::TM * 2048 + r16 * 128 + (((lane >> 4) ^ x_swizzle(r16)) << 4);
+    auto read = [&](const uint8_t *x, const uint8_t *wt, int odd, int to) {
+        const uint8_t *wl = wt + wn * S::TN * 1024 + lane * 16;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            i32x4 xf[S::TM], wf[S::TN];
+        for (int j = 0; j < S::TN; j++)
+            wf[to][j] = *(const i32x4 *)(wl + j * 1024);
 #pragma unroll
-            for (int j = 0; j < S::TN; j++)
-                wf[j] = *(const i32x4 *)(wl + j * 2048 + h * 1024);
-#pragma unroll
-            for (int i = 0; i < S::TM; i++)
-                xf[i] = *(const i32x4 *)(xl + i * 2048 + h * 1024);
-#pragma unroll
-            for (int i = 0; i < S::TM; i++)
-#pragma unroll
-                for (int j = 0; j < S::TN; j++)
-                    acc[i][j] = mfma_i8(wf[j], xf[i], acc[i][j]);
-        }
+        for (int i = 0; i < S::TM; i++)
+            xf[to][i] = *(const i32x4 *)(x + (xl ^ (odd << 6)) + i * 2048);
     };
 #pragma unroll
     for (int i = 0; i < S::TM; i++)
 #pragma unroll
         for (int j = 0; j < S::TN; j++)
             acc[i][j] = i32x4{0, 0, 0, 0};
-    load(k0, st0);
-    __syncthreads();
-    for (int kt = k0; kt < k1; kt += 2) {
-        if (kt + 1 < k1)
-            load(kt + 1, st1);
-        compute(st0);
-        __syncthreads();
-        if (kt + 1 < k1) {
-            if (kt + 2 < k1)
-                load(kt + 2, st0);
-            compute(st1);
-            __syncthreads();
+    // in the order that the loop keeps: a step's weights, then (odd steps) codes
+    load_x(k0, lds.x[0]);
+    load_w(k0, lds.w[0]);
+    load_w(k0 + 1, lds.w[1]);
+    load_x(k0 + 2, lds.x[1]);
+    load_w(k0 + 2, lds.w[2]);
+    load_w(k0 + 3, lds.w[3]);
+    step_barrier<S::XPW + 3 * S::WPW>();
+    read(lds.x[0], lds.w[0], 0, 0);
+    for (int kt = k0; kt < k1; kt += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            // Even steps wait for the next step's weights, with two steps'
+            // weights and one load of codes issued after them; odd steps for
+            // the next double step of codes too, with one step's weights after.
+            if (u & 1)
+                step_barrier<S::WPW>();
+            else
+                step_barrier<S::XPW + 2 * S::WPW>();
+            load_w(kt + u + 4, lds.w[u]);
+            if (u & 1)
+                load_x(kt + u + 3, lds.x[u / 2]);
+            read(lds.x[(u + 1) / 2 % 2], lds.w[(u + 1) % 4], (u + 1) & 1, (u + 1) & 1);
+#pragma unroll
+            for (int i = 0; i < S::TM; i++)
+#pragma unroll
+                for (int j = 0; j < S::TN; j++)
+                    acc[i][j] = mfma_i8(wf[u & 1][j], xf[u & 1][i], acc[i][j]);
+            if (u & 1)
+                ti_interleave<S::WPW + S::XPW, S::TM + S::TN, S::TM * S::TN>();
+            else
+                ti_interleave<S::WPW, S::TM + S::TN, S::TM * S::TN>();
         }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load outlives the workgroup's LDS
 }
 
 // Workgroup id -> tile: consecutive ids go to the 8 XCDs in turn, so an XCD's
@@ -164,20 +235,19 @@ __device__ __forceinline__ int xcd_order(int id, int n)
 }
 
 template <typename S, bool DUAL, int OUTT>
-__global__ __launch_bounds__(64 * S::NW, S::NW == 8 ? 2 : 2) void i8_tiled_kernel(I8Args a, int mtiles, int ntiles,
+__global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int mtiles, int ntiles,
                                                                                 int split, int32_t *part)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[S::STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t st1[S::STAGE];
+    TI_LDS(S, lds);
     const int t = xcd_order(blockIdx.x, gridDim.x);
     const int tile = t / split, piece = t % split;
     const int mt = tile % mtiles, nt = tile / mtiles;
-    const int steps = a.S / 2, per = (steps + split - 1) / split;
+    const int steps = a.S, per = (steps / 4 + split - 1) / split * 4;
     const int k0 = piece * per, k1 = min(steps, k0 + per);
     const int64_t row0 = (int64_t)mt * S::BM;
     const int rows = min(S::BM, (int)(a.B - row0));
     i32x4 acc[S::TM][S::TN];
-    ti_tile_sums<S, DUAL>(a, a.w, row0, rows, nt, k0, k1, st0, st1, acc);
+    ti_tile_sums<S, DUAL>(a, a.w, row0, rows, nt, k0, k1, lds, acc);
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     if (split > 1) {
         i32x4 *p = (i32x4 *)part + ((int64_t)t * S::NW + wid) * S::TM * S::TN * 64;
@@ -224,8 +294,7 @@ __global__ __launch_bounds__(64) void i8_tiled_reduce_kernel(I8Args a, int mtile
 template <typename S, bool DUAL, int OUTT>
 __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args a, I8Groups grp, int ntiles)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[S::STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t st1[S::STAGE];
+    TI_LDS(S, lds);
     __shared__ int wsum[S::NW], found[4];
     constexpr int NT = 64 * S::NW;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
@@ -278,7 +347,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args 
     const int rows = min(S::BM, __builtin_amdgcn_readfirstlane(found[2]) - row0);
     const uint8_t *w = uniform_ptr(grp.wtab[e]);
     i32x4 acc[S::TM][S::TN];
-    ti_tile_sums<S, DUAL>(a, w, row0, rows, nt, 0, a.S / 2, st0, st1, acc);
+    ti_tile_sums<S, DUAL>(a, w, row0, rows, nt, 0, a.S, lds, acc);
 #pragma unroll
     for (int i = 0; i < S::TM; i++)
         ti_store<S, DUAL, OUTT>(a, w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc[i]);
@@ -297,11 +366,11 @@ I8TiCfg i8_tiled_cfg(const I8Args &a, bool split)
     c.mtiles = (a.B + c.BM - 1) / c.BM;
     c.ntiles = (cols + c.BN - 1) / c.BN;
     const int64_t tiles = (int64_t)c.mtiles * c.ntiles;
-    const int steps = a.S / 2;
+    const int steps = a.S / 4;  // in fours, as the kernel walks them
     c.split = 1;
     if (split && tiles < 256) {
         int s = (int)(512 / tiles);
-        s = s > steps / 4 ? steps / 4 : s;
+        s = s > steps / 2 ? steps / 2 : s;
         s = s < 1 ? 1 : s;
         const int per = (steps + s - 1) / s;
         c.split = (steps + per - 1) / per;  // no empty piece

@@ -8,7 +8,7 @@
 // order, so the scales of a slab are one 64-byte (128-byte for NVFP4) piece
 // of a cache line; NVFP4 adds a 256-byte tensor-scale record.  INT8 slabs
 // hold 64 weights along K whose chunk L is lane L's operand of one 16x16x64
-// int8 MFMA (row L % 16, k = 16 * (L / 16) + 0..15); K is padded to two slabs
+// int8 MFMA (row L % 16, k = 16 * (L / 16) + 0..15); K is padded to four slabs
 // and one fp32 scale a row follows the codes.
 #pragma once
 #include <stdint.h>
@@ -75,7 +75,7 @@ static inline bool make_layout(int fmt, int64_t N, int64_t K, Layout *L)
     L->blk = block_of(fmt);
     L->KS = slab_k(fmt);
     L->Np = round_up(N, 16);
-    L->Kp = round_up(K, fmt == FMT_I8 ? 2 * L->KS : L->KS);
+    L->Kp = round_up(K, fmt == FMT_I8 ? 4 * L->KS : L->KS);
     L->S = L->Kp / L->KS;
     L->RT = L->Np / 16;
     int64_t codes = L->RT * L->S * 1024;

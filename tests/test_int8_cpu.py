@@ -18,7 +18,7 @@ def test_pack_layout_roundtrip():
         codes = rng.integers(-128, 128, (n, k)).astype(np.int8)
         scales = rng.standard_normal(n).astype(np.float32)
         buf = q.pack("int8", n, k, codes, scales)
-        npad, kpad = -(-n // 16) * 16, -(-k // 128) * 128
+        npad, kpad = -(-n // 16) * 16, -(-k // 256) * 256
         soff = -(-npad * kpad // 256) * 256
         assert buf.size == q.weight_bytes("int8", n, k) == soff + -(-npad * 4 // 256) * 256
         # [row tile][slab][k group][row][16 codes]
