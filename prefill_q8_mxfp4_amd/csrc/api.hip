@@ -599,7 +599,8 @@ static int64_t i8_part_bytes(const qgemm_plan *plan, int64_t B)
 {
     if (i8_tier(plan, B) != QGEMM_TIER_TILED)
         return 0;
-    return round_up(i8_tiled_cfg(i8_args(plan->p, B, nullptr, nullptr, 0, nullptr, nullptr), true).part_bytes, 256);
+    return round_up(i8_tiled_cfg(i8_args(plan->p, B, nullptr, nullptr, 0, nullptr, nullptr), true,
+                                 plan->p.kn.ti_bm, plan->p.kn.ti_split).part_bytes, 256);
 }
 
 static int64_t i8_code_stride(const Problem &p) { return round_up(p.K, 16); }
@@ -942,9 +943,9 @@ static int i8_product(const qgemm_plan *plan, const I8Args &a, uint8_t *part, in
     if (i8_tier(plan, a.B) == QGEMM_TIER_SKINNY) {
         e = launch_i8_small(a, plan->p.out, st);
     } else {
-        I8TiCfg c = i8_tiled_cfg(a, part != nullptr);
+        I8TiCfg c = i8_tiled_cfg(a, part != nullptr, plan->p.kn.ti_bm, plan->p.kn.ti_split);
         if (c.part_bytes > part_bytes)
-            c = i8_tiled_cfg(a, false);
+            c = i8_tiled_cfg(a, false, plan->p.kn.ti_bm, 0);
         e = launch_i8_tiled(a, c, (int32_t *)part, plan->p.out, st);
     }
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run: kernel launch");
@@ -1387,10 +1388,9 @@ int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const 
     const I8Args a = i8_args(plan->p, T, nullptr, codes, ldc, scales, y);
     const bool small = grouped_tier(plan, E, T) == QGEMM_TIER_SKINNY;
     // row groups of 16 channels at least, or tiles of 128 x 128 at least
-    if (small ? E * ((int64_t)a.RT + 1) > 0x7FFFFFFFll : (T / 64 + (E < T ? E : T)) * ((int64_t)a.RT / 4 + 1) > 0x7FFFFFFFll)
+    if (small ? E * ((int64_t)a.RT + 1) > 0x7FFFFFFFll : (T / 64 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 4 + 1) > 0x7FFFFFFFll)
         return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: grid too large");
-    const hipError_t e = small ? launch_i8_small_grouped(a, g, plan->p.out, (hipStream_t)stream)
-                               : launch_i8_tiled_grouped(a, g, plan->p.out, (hipStream_t)stream);
+    const hipError_t e = launch_i8_grouped(a, g, plan->p.kn.ti_bm ? plan->p.kn.ti_bm : small ? 16 : 128, plan->p.out, (hipStream_t)stream);
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run_grouped_codes: kernel launch");
 }
 

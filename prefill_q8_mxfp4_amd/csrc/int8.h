@@ -97,8 +97,7 @@ hipError_t launch_i8_pack(const Layout &L, const int8_t *codes, const float *sca
 
 // ---- int8_small.hip: few rows, weights streamed into the operands
 hipError_t launch_i8_small(const I8Args &a, int outt, hipStream_t st);
-hipError_t launch_i8_small_grouped(const I8Args &a, const I8Groups &g, int outt, hipStream_t st);
-constexpr int I8_SMALL_MAX_B = 64;  // largest B of the automatic choice
+constexpr int I8_SMALL_MAX_B = 80;  // largest B of the automatic choice
 
 // ---- int8_tiled.hip: many rows, tiles through LDS
 struct I8TiCfg {
@@ -107,9 +106,10 @@ struct I8TiCfg {
     int split;           // workgroups along K for each tile
     int64_t part_bytes;  // int32 partial tiles (0 without a split)
 };
-I8TiCfg i8_tiled_cfg(const I8Args &a, bool split);
+I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int bm, int forced);
 hipError_t launch_i8_tiled(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st);
-hipError_t launch_i8_tiled_grouped(const I8Args &a, const I8Groups &g, int outt, hipStream_t st);
+// rows sorted by expert, tiles of bm (16, 32, 64 or 128) rows x 128 channels
+hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int bm, int outt, hipStream_t st);
 
 // ---- route.hip
 constexpr uint32_t DEV_BAD_ROUTE = 4u;  // a position past the rows

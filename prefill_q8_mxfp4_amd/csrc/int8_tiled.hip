@@ -26,13 +26,19 @@ template <int WM_, int WN_, int TM_, int TN_>
 struct TiShape {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // waves, and 16-wide tiles a wave
     static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
-    static constexpr int XC = BM / 8, WC = BN / 16;     // KBs of a double step of codes, of a step of weights
+    // KBs of a double step of codes (the same number for each wave: copies of
+    // the last row past BM) and of a step of weights
+    static constexpr int XC = (BM / 8 + NW - 1) / NW * NW, WC = BN / 16;
     static constexpr int XPW = XC / NW, WPW = WC / NW;  // of them a wave loads
     static constexpr int XST = XC * 1024, WST = WC * 1024;
     static_assert(XC % NW == 0 && WC % NW == 0, "whole KBs a wave");
 };
 using TiBig = TiShape<2, 4, 8, 4>;  // 256 x 256, 8 waves of 128 x 64
 using TiMid = TiShape<2, 2, 4, 4>;  // 128 x 128, 4 waves of 64 x 64
+using TiWide = TiShape<1, 4, 5, 4>;  // 80 x 256, 4 waves of 80 x 64
+using TiLow = TiShape<2, 2, 2, 4>;  // 64 x 128, 4 waves of 32 x 64
+using TiFew = TiShape<1, 4, 2, 2>;  // 32 x 128, 4 waves of 32 x 32
+using TiOne = TiShape<1, 4, 1, 2>;  // 16 x 128, 4 waves of 16 x 32
 
 __device__ __forceinline__ void load_chunk(__amdgpu_buffer_rsrc_t r, uint8_t *lds, int voff, int soff)
 {
@@ -288,9 +294,11 @@ __global__ __launch_bounds__(64) void i8_tiled_reduce_kernel(I8Args a, int mtile
     ti_store<S, DUAL, OUTT>(a, a.w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc);
 }
 
-// Rows sorted by expert: workgroup t of the grid's bound takes the t'th
-// (expert, row tile, weight tile), weight tiles fastest, found by a scan of the
-// experts' row-tile counts; those past the real count leave.
+// Rows sorted by expert: the grid covers a bound on the experts' row tiles, each
+// with its weight tiles; a workgroup finds its expert by a scan of the experts'
+// row-tile counts, and those past the real count leave.  Row tiles are dealt to
+// the XCDs in turn (the real ones are the first of the bound, so runs of them
+// would leave half of the XCDs idle), a row tile's weight tiles to one XCD.
 template <typename S, bool DUAL, int OUTT>
 __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args a, I8Groups grp, int ntiles)
 {
@@ -298,24 +306,31 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args 
     __shared__ int wsum[S::NW], found[4];
     constexpr int NT = 64 * S::NW;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-    const int t = xcd_order(blockIdx.x, gridDim.x);
-    const int mt = t / ntiles, nt = t % ntiles;  // row tile over all experts
+    const int loc = blockIdx.x / 8;
+    const int mt = loc / ntiles * 8 + blockIdx.x % 8, nt = loc % ntiles;  // row tile over all experts
+    // PER neighbouring experts a thread: up to NT * PER of them with one wait for
+    // their offsets
+    constexpr int PER = 4;
     if (tid == 0)
         found[0] = -1;
     int carry = 0;
-    for (int e0 = 0; e0 < grp.E; e0 += NT) {
-        const int e = e0 + tid;
-        int lo = 0, hi = 0;
-        if (e < grp.E) {
-            lo = grp.off[e];
-            hi = grp.off[e + 1];
-            if (lo < 0 || hi < lo || hi > a.B || (e == 0 && lo != 0)) {
-                lo = hi = 0;
+    for (int e0 = 0; e0 < grp.E; e0 += NT * PER) {
+        int off[PER + 1], cnt[PER], v = 0;
+#pragma unroll
+        for (int k = 0; k <= PER; k++)
+            off[k] = grp.off[min(e0 + tid * PER + k, grp.E)];
+#pragma unroll
+        for (int k = 0; k < PER; k++) {
+            const int e = e0 + tid * PER + k;
+            if (e < grp.E && (off[k] < 0 || off[k + 1] < off[k] || off[k + 1] > a.B || (e == 0 && off[k] != 0))) {
+                cnt[k] = 0;
                 if (blockIdx.x == 0)
                     __hip_atomic_fetch_or(grp.status, DEV_BAD_OFFSETS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            } else {
+                cnt[k] = (off[k + 1] - off[k] + S::BM - 1) / S::BM;  // 0 past the last expert
             }
+            v += cnt[k];
         }
-        const int v = (hi - lo + S::BM - 1) / S::BM;
         int s = v;
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(s, d);
@@ -325,16 +340,19 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args 
         if (lane == 63)
             wsum[wid] = s;
         __syncthreads();
-        int before = carry;
+        int first = carry + s - v;
         for (int k = 0; k < S::NW; k++) {
-            before += k < wid ? wsum[k] : 0;
+            first += k < wid ? wsum[k] : 0;
             carry += wsum[k];
         }
-        const int first = before + s - v;
-        if (mt >= first && mt < first + v) {
-            found[0] = e;
-            found[1] = lo + (mt - first) * S::BM;
-            found[2] = hi;
+#pragma unroll
+        for (int k = 0; k < PER; k++) {
+            if (mt >= first && mt < first + cnt[k]) {
+                found[0] = e0 + tid * PER + k;
+                found[1] = off[k] + (mt - first) * S::BM;
+                found[2] = off[k + 1];
+            }
+            first += cnt[k];
         }
         __syncthreads();
         if (found[0] >= 0)
@@ -357,12 +375,13 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args 
 
 // Whole tiles of the larger shape when they fill the chip, else the smaller
 // one, K split so that at least a round of tiles runs.
-I8TiCfg i8_tiled_cfg(const I8Args &a, bool split)
+I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int bm, int forced)
 {
     I8TiCfg c;
     const int cols = a.Nh ? 2 * a.Nh : a.N;
     const int64_t big = (int64_t)((a.B + 255) / 256) * ((cols + 255) / 256);
-    c.BM = c.BN = big >= 192 ? 256 : 128;
+    c.BM = bm ? bm : big >= 192 ? 256 : 128;
+    c.BN = c.BM == 80 || c.BM == 256 ? 256 : 128;
     c.mtiles = (a.B + c.BM - 1) / c.BM;
     c.ntiles = (cols + c.BN - 1) / c.BN;
     const int64_t tiles = (int64_t)c.mtiles * c.ntiles;
@@ -372,6 +391,7 @@ I8TiCfg i8_tiled_cfg(const I8Args &a, bool split)
         int s = (int)(512 / tiles);
         s = s > steps / 2 ? steps / 2 : s;
         s = s < 1 ? 1 : s;
+        if (forced) s = forced > steps ? steps : forced;
         const int per = (steps + s - 1) / s;
         c.split = (steps + per - 1) / per;  // no empty piece
     }
@@ -405,21 +425,24 @@ static void tiled_shape(const I8Args &a, const I8TiCfg &c, int32_t *part, int ou
 
 hipError_t launch_i8_tiled(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st)
 {
-    if (c.BM == 256)
-        tiled_shape<TiBig>(a, c, part, outt, st);
-    else
-        tiled_shape<TiMid>(a, c, part, outt, st);
+    switch (c.BM) {
+    case 32: tiled_shape<TiFew>(a, c, part, outt, st); break;
+    case 64: tiled_shape<TiLow>(a, c, part, outt, st); break;
+    case 80: tiled_shape<TiWide>(a, c, part, outt, st); break;
+    case 128: tiled_shape<TiMid>(a, c, part, outt, st); break;
+    default: tiled_shape<TiBig>(a, c, part, outt, st); break;
+    }
     return hipGetLastError();
 }
 
-hipError_t launch_i8_tiled_grouped(const I8Args &a, const I8Groups &g, int outt, hipStream_t st)
+template <typename S>
+static void grouped_go(const I8Args &a, const I8Groups &g, int outt, hipStream_t st)
 {
-    using S = TiMid;
     const int cols = a.Nh ? 2 * a.Nh : a.N;
     const int ntiles = (cols + S::BN - 1) / S::BN;
     // an expert adds at most one partial tile, and at most B experts have rows
     const int64_t tiles = a.B / S::BM + (g.E < a.B ? g.E : a.B);
-    const dim3 grid((unsigned)(tiles * ntiles)), blk(64 * S::NW);
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * ntiles)), blk(64 * S::NW);
     if (a.Nh && outt == OUT_F32)
         hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, true, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
     else if (a.Nh)
@@ -428,6 +451,16 @@ hipError_t launch_i8_tiled_grouped(const I8Args &a, const I8Groups &g, int outt,
         hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, false, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
     else
         hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, false, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
+}
+
+hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int bm, int outt, hipStream_t st)
+{
+    switch (bm) {
+    case 16: grouped_go<TiOne>(a, g, outt, st); break;
+    case 32: grouped_go<TiFew>(a, g, outt, st); break;
+    case 64: grouped_go<TiLow>(a, g, outt, st); break;
+    default: grouped_go<TiMid>(a, g, outt, st); break;
+    }
     return hipGetLastError();
 }
 
