@@ -53,6 +53,7 @@ static void read_knobs(Knobs *k)
     k->ti_bm = env_int("QGEMM_TI_BM", 0);
     k->ti_split = env_int("QGEMM_TI_SPLIT", 0);
     k->ti_waves = env_int("QGEMM_TI_WAVES", 0);
+    k->i8_shape = env_int("QGEMM_I8_SHAPE", 0);
     k->xlocal = env_int("QGEMM_ST_XLOCAL", -1) == 0 ? 0 : -1;
     k->fp32_terms = 3;
     k->xcc_fake = 0;
@@ -547,7 +548,7 @@ static int i8_tier(const qgemm_plan *plan, int64_t B)
 {
     if (plan->forced_tier)
         return plan->forced_tier;
-    return B <= I8_SMALL_MAX_B ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
+    return i8_small_wins(B, plan->p.N) ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
 }
 
 static int choose_tier(const qgemm_plan *plan, int64_t B)
@@ -600,7 +601,7 @@ static int64_t i8_part_bytes(const qgemm_plan *plan, int64_t B)
     if (i8_tier(plan, B) != QGEMM_TIER_TILED)
         return 0;
     return round_up(i8_tiled_cfg(i8_args(plan->p, B, nullptr, nullptr, 0, nullptr, nullptr), true,
-                                 plan->p.kn.ti_bm, plan->p.kn.ti_split).part_bytes, 256);
+                                 plan->p.kn.i8_shape, plan->p.kn.ti_split).part_bytes, 256);
 }
 
 static int64_t i8_code_stride(const Problem &p) { return round_up(p.K, 16); }
@@ -943,9 +944,9 @@ static int i8_product(const qgemm_plan *plan, const I8Args &a, uint8_t *part, in
     if (i8_tier(plan, a.B) == QGEMM_TIER_SKINNY) {
         e = launch_i8_small(a, plan->p.out, st);
     } else {
-        I8TiCfg c = i8_tiled_cfg(a, part != nullptr, plan->p.kn.ti_bm, plan->p.kn.ti_split);
+        I8TiCfg c = i8_tiled_cfg(a, part != nullptr, plan->p.kn.i8_shape, plan->p.kn.ti_split);
         if (c.part_bytes > part_bytes)
-            c = i8_tiled_cfg(a, false, plan->p.kn.ti_bm, 0);
+            c = i8_tiled_cfg(a, false, plan->p.kn.i8_shape, 0);
         e = launch_i8_tiled(a, c, (int32_t *)part, plan->p.out, st);
     }
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run: kernel launch");
@@ -1121,7 +1122,7 @@ static int grouped_tier(const qgemm_plan *plan, int64_t E, int64_t T)
     if (plan->forced_tier == QGEMM_TIER_GEMV)
         return 0;
     if (p.fmt == FMT_I8)
-        return plan->forced_tier ? plan->forced_tier : T < 64 * E ? QGEMM_TIER_SKINNY : QGEMM_TIER_TILED;
+        return QGEMM_TIER_TILED;
     const int64_t xsz = p.act == QGEMM_F32 ? 4 : 2;
     const bool small_ok = p.math == QGEMM_MATH_BF16 && T * p.K * xsz < (1ll << 31) &&
                           E * moe_groups(p) <= 0x7FFFFFFFll && moe_groups_per_wg(p, E) >= 1;
@@ -1386,11 +1387,12 @@ int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const 
     if (!g.status)
         return fail(QGEMM_EHIP, "qgemm_run_grouped_codes: no device status word");
     const I8Args a = i8_args(plan->p, T, nullptr, codes, ldc, scales, y);
-    const bool small = grouped_tier(plan, E, T) == QGEMM_TIER_SKINNY;
-    // row groups of 16 channels at least, or tiles of 128 x 128 at least
-    if (small ? E * ((int64_t)a.RT + 1) > 0x7FFFFFFFll : (T / 64 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 4 + 1) > 0x7FFFFFFFll)
+    const int forced = plan->p.kn.i8_shape;
+    const int shape = forced == I8_64x128 || forced >= I8_32x128 ? forced : i8_grouped_shape(E, T);
+    // row tiles of 32 at least, weight tiles of 128
+    if ((T / 32 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 8 + 1) > 0x7FFFFFFFll)
         return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: grid too large");
-    const hipError_t e = launch_i8_grouped(a, g, plan->p.kn.ti_bm ? plan->p.kn.ti_bm : small ? 16 : 128, plan->p.out, (hipStream_t)stream);
+    const hipError_t e = launch_i8_grouped(a, g, shape, plan->p.out, (hipStream_t)stream);
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run_grouped_codes: kernel launch");
 }
 

@@ -356,6 +356,7 @@ struct Knobs {
     int vf_swiglu_maxb;    // largest B the fused gate+up epilogue takes the verify kernel at (QGEMM_VF_SWIGLU_MAXB)
     int ti_bm, ti_split;   // large-batch row-tile height, K splits (QGEMM_TI_BM, QGEMM_TI_SPLIT)
     int ti_waves;          // large-batch waves per workgroup, 4 or 8 (QGEMM_TI_WAVES; 0 = default)
+    int i8_shape;          // tile of INT8 products, an I8Shape (QGEMM_I8_SHAPE; 0: by cost; one a call cannot take is ignored)
     int xlocal;            // -1 the probe decides, 0 device-coherent, 1 forced (debug)
     int fp32_terms;        // activation terms of fp32-faithful math (3; debug 1..3)
     int xcc_fake;          // debug: odd K splits report the next XCC to the placement check

@@ -53,28 +53,31 @@ __device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *p)
     return (const uint8_t *)(((uint64_t)hi << 32) | lo);
 }
 
-// Four neighbouring outputs y[b][n .. n+3] of one lane, from n0 = the first
-// channel; `vec`: ncols is a multiple of 4, so the four are one aligned store.
+// Four neighbouring outputs of one lane: one store, which gfx950 takes at any
+// alignment; _part: only the first `left` of them are inside.
 template <int OUTT>
-__device__ __forceinline__ void i8_store4(void *y, int64_t row, int ncols, int n, bool vec, f32x4 v)
+__device__ __forceinline__ void i8_put4(void *to, f32x4 v)
 {
-    const int64_t at = row * ncols + n;
-    if (vec) {
-        if (n < ncols) {
-            if constexpr (OUTT == OUT_F32) {
-                *(f32x4 *)((float *)y + at) = v;
-            } else {
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                bf16x4 o;
-                o[0] = (__bf16)v[0]; o[1] = (__bf16)v[1]; o[2] = (__bf16)v[2]; o[3] = (__bf16)v[3];
-                *(bf16x4 *)((__bf16 *)y + at) = o;
-            }
-        }
+    if constexpr (OUTT == OUT_F32) {
+        __builtin_memcpy(to, &v, 16);
+    } else {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        bf16x4 o;
+        o[0] = (__bf16)v[0]; o[1] = (__bf16)v[1]; o[2] = (__bf16)v[2]; o[3] = (__bf16)v[3];
+        __builtin_memcpy(to, &o, 8);
+    }
+}
+
+template <int OUTT>
+__device__ __forceinline__ void i8_put4_part(void *to, f32x4 v, int left)
+{
+    if (left >= 4) {
+        i8_put4<OUTT>(to, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (n + i < ncols)
-                store_out<OUTT>(y, at + i, v[i]);
+        for (int i = 0; i < 3; i++)
+            if (i < left)
+                store_out<OUTT>(to, i, v[i]);
     }
 }
 
@@ -97,19 +100,25 @@ hipError_t launch_i8_pack(const Layout &L, const int8_t *codes, const float *sca
 
 // ---- int8_small.hip: few rows, weights streamed into the operands
 hipError_t launch_i8_small(const I8Args &a, int outt, hipStream_t st);
-constexpr int I8_SMALL_MAX_B = 80;  // largest B of the automatic choice
+bool i8_small_wins(int64_t B, int64_t N);  // the automatic choice
 
 // ---- int8_tiled.hip: many rows, tiles through LDS
+enum I8Shape {  // batch rows x channels of a tile
+    I8_32x32 = 1, I8_32x64, I8_64x64, I8_64x128, I8_128x128R, I8_128x256, I8_256x256,
+    I8_32x128, I8_128x128,  // routed rows (and 64 x 128)
+};
 struct I8TiCfg {
-    int BM, BN;          // batch rows and weight rows of a tile
+    int shape;
     int mtiles, ntiles;
     int split;           // workgroups along K for each tile
     int64_t part_bytes;  // int32 partial tiles (0 without a split)
 };
-I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int bm, int forced);
+// The shape and K split of least cost; shape, pieces: forced where not 0 (a
+// split only with `split`: room for its partial tiles).
+I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int shape, int pieces);
 hipError_t launch_i8_tiled(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st);
-// rows sorted by expert, tiles of bm (16, 32, 64 or 128) rows x 128 channels
-hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int bm, int outt, hipStream_t st);
+int i8_grouped_shape(int64_t E, int64_t T);
+hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int shape, int outt, hipStream_t st);
 
 // ---- route.hip
 constexpr uint32_t DEV_BAD_ROUTE = 4u;  // a position past the rows

@@ -5,8 +5,8 @@
 // lane L of v_mfma_i32_16x16x64_i8, and lane L's 16 bytes of a row's codes
 // (row L % 16, k group L / 16) are the B operand, so nothing is decoded or
 // shuffled.  Reading the weights is the bound: a workgroup owns R row tiles and
-// all rows, its waves take the slabs of those tiles two at a time (the codes'
-// two 64-byte halves of a cache line) and keep SLOTS such pairs in flight in
+// 16 rows, its waves take the slabs of those tiles two at a time (the codes' two
+// 64-byte halves of a cache line) and keep SLOTS such pairs in flight in
 // registers.  The waves' int32 sums meet in LDS: sums of whole numbers, so the
 // split changes no bit.  A lane ends with four neighbouring channels of one row.
 #include "int8.h"
@@ -29,12 +29,12 @@ __device__ __forceinline__ int sm_tile(const I8Args &a, int g, int r)
     }
 }
 
-template <int R, int CG, int SLOTS, bool DUAL, int OUTT>
+template <int R, int SLOTS, bool DUAL, int OUTT>
 __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
 {
-    __shared__ i32x4 red[2][SM_W * R * 64];
-    const int g = blockIdx.x, row0 = blockIdx.y * 16 * CG;
-    const int rows = min(16 * CG, a.B - row0);
+    __shared__ i32x4 red[SM_W * R * 64];
+    const int g = blockIdx.x, row0 = blockIdx.y * 16;
+    const int rows = min(16, a.B - row0);
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, kg = lane >> 4;
@@ -45,21 +45,16 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
         wt[r] = a.w + sm_tile<R, DUAL>(a, g, r) * tile_bytes;
     const uint8_t *xbase = (const uint8_t *)a.codes + (int64_t)row0 * a.ldc;
     const int64_t xbytes = (int64_t)rows * a.ldc;
-    int xo[CG];
-#pragma unroll
-    for (int c = 0; c < CG; c++)  // rows past the last read row 0: their columns are never stored
-        xo[c] = (c * 16 + c16 < rows ? (c * 16 + c16) * a.ldc : 0) + kg * 16;
-    i32x4 acc[R][CG];
+    const int xo = (c16 < rows ? c16 * a.ldc : 0) + kg * 16;  // rows past the last: row 0, never stored
+    i32x4 acc[R];
 #pragma unroll
     for (int r = 0; r < R; r++)
-#pragma unroll
-        for (int c = 0; c < CG; c++)
-            acc[r][c] = i32x4{0, 0, 0, 0};
+        acc[r] = i32x4{0, 0, 0, 0};
 
     // The i'th pair of slabs of this wave (S is even) into a slot; past the
     // last one zeros from empty resources, so that every step issues the same
     // loads and the waits for the slots are exact.
-    i32x4 wv[SLOTS][2][R], xv[SLOTS][2][CG];
+    i32x4 wv[SLOTS][2][R], xv[SLOTS][2];
     auto load = [&](int i, int slot) {
         const int s = (i * SM_W + wid) * 2;
         const bool live = s < a.S;
@@ -70,9 +65,7 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
             for (int r = 0; r < R; r++)
                 wv[slot][h][r] = __builtin_bit_cast(
                     i32x4, bload16_nt(make_rsrc(wt[r], live ? tile_bytes : 0), lane * 16, live ? (s + h) << 10 : 0));
-#pragma unroll
-            for (int c = 0; c < CG; c++)
-                xv[slot][h][c] = __builtin_bit_cast(i32x4, bload16(xr, xo[c] + ((s + h) << 6), 0));
+            xv[slot][h] = __builtin_bit_cast(i32x4, bload16(xr, xo + ((s + h) << 6), 0));
         }
     };
     const int n = (a.S / 2 + SM_W - 1) / SM_W;
@@ -86,9 +79,7 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
         for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int r = 0; r < R; r++)
-#pragma unroll
-                for (int c = 0; c < CG; c++)
-                    acc[r][c] = mfma_i8(wv[u][h][r], xv[u][h][c], acc[r][c]);
+                acc[r] = mfma_i8(wv[u][h][r], xv[u][h], acc[r]);
     };
     for (int i = SLOTS; i < n; i += SLOTS) {
 #pragma unroll
@@ -103,87 +94,69 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
     for (int u = 0; u < SLOTS; u++)
         multiply(u);
 
-    // a row group at a time through one of two buffers: one barrier each
+#pragma unroll
+    for (int r = 0; r < R; r++)
+        red[(wid * R + r) * 64 + lane] = acc[r];
+    __syncthreads();
     constexpr int RO = DUAL ? R / 2 : R;  // output tiles of a workgroup
-    const bool vec = (a.ncols & 3) == 0;
     const float *ws = (const float *)(a.w + a.scale_off);
+    if (wid < RO) {
+        auto sum = [&](int r) {
+            i32x4 v = red[r * 64 + lane];
 #pragma unroll
-    for (int c = 0; c < CG; c++) {
-        i32x4 *buf = red[c & 1];
+            for (int k = 1; k < SM_W; k++)
+                v += red[(k * R + r) * 64 + lane];
+            return v;
+        };
+        const int n = (g * RO + wid) * 16 + kg * 4;
+        const i32x4 s = sum(wid);
+        i32x4 up = s;
+        if constexpr (DUAL)
+            up = sum(wid + RO);
+        if (c16 < rows && n < a.ncols) {
+            const float xs = a.xs[row0 + c16];
+            const f32x4 t = *(const f32x4 *)(ws + n);
+            f32x4 out;
 #pragma unroll
-        for (int r = 0; r < R; r++)
-            buf[(wid * R + r) * 64 + lane] = acc[r][c];
-        __syncthreads();
-        // output tile o of this row group: the waves in turn, over the row groups
-        for (int o = (wid + SM_W - c * RO % SM_W) % SM_W; o < RO; o += SM_W) {
-            auto sum = [&](int r) {
-                i32x4 v = buf[r * 64 + lane];
-#pragma unroll
-                for (int k = 1; k < SM_W; k++)
-                    v += buf[(k * R + r) * 64 + lane];
-                return v;
-            };
-            const int nn = (g * RO + o) * 16 + kg * 4;
-            const int b = c * 16 + c16;
-            const i32x4 s = sum(o);
-            i32x4 up = s;
-            if constexpr (DUAL)
-                up = sum(o + RO);
-            if (b < rows && nn < a.ncols) {
-                const float xs = a.xs[row0 + b];
-                const f32x4 t = *(const f32x4 *)(ws + nn);
-                f32x4 out;
+            for (int i = 0; i < 4; i++)
+                out[i] = (float)s[i] * xs * t[i];
+            if constexpr (DUAL) {
+                const f32x4 tu = *(const f32x4 *)(ws + a.Nh + n);
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    out[i] = (float)s[i] * xs * t[i];
-                if constexpr (DUAL) {
-                    const f32x4 tu = *(const f32x4 *)(ws + a.Nh + nn);
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        out[i] = silu(out[i]) * ((float)up[i] * xs * tu[i]);
-                }
-                i8_store4<OUTT>(a.y, row0 + b, a.ncols, nn, vec, out);
+                    out[i] = silu(out[i]) * ((float)up[i] * xs * tu[i]);
             }
+            i8_put4_part<OUTT>((uint8_t *)a.y + ((int64_t)(row0 + c16) * a.ncols + n) * (OUTT == OUT_F32 ? 4 : 2),
+                               out, a.ncols - n);
         }
     }
 }
 
-template <int R, int CG, int SLOTS>
+template <int R, int SLOTS, bool DUAL>
 static void small_go(const I8Args &a, int outt, hipStream_t st)
 {
-    const int groups = a.Nh ? (a.Nh / 16 + (R + 1) / 2 - 1) / ((R + 1) / 2) : (a.RT + R - 1) / R;
-    const dim3 grid((unsigned)groups, (unsigned)((a.B + 16 * CG - 1) / (16 * CG))), blk(64 * SM_W);
-    if constexpr (R % 2 == 0) {
-        if (a.Nh && outt == OUT_F32)
-            hipLaunchKernelGGL((i8_small_kernel<R, CG, SLOTS, true, OUT_F32>), grid, blk, 0, st, a);
-        else if (a.Nh)
-            hipLaunchKernelGGL((i8_small_kernel<R, CG, SLOTS, true, OUT_BF16>), grid, blk, 0, st, a);
-        if (a.Nh)
-            return;
-    }
+    const int groups = DUAL ? a.Nh / 16 : (a.RT + R - 1) / R;
+    const dim3 grid((unsigned)groups, (unsigned)((a.B + 15) / 16)), blk(64 * SM_W);
     if (outt == OUT_F32)
-        hipLaunchKernelGGL((i8_small_kernel<R, CG, SLOTS, false, OUT_F32>), grid, blk, 0, st, a);
+        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_F32>), grid, blk, 0, st, a);
     else
-        hipLaunchKernelGGL((i8_small_kernel<R, CG, SLOTS, false, OUT_BF16>), grid, blk, 0, st, a);
+        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_BF16>), grid, blk, 0, st, a);
 }
+
+// Up to two rows any weight, up to 16 rows one of 8192 channels or more.
+// Measured against the tiled kernel's best shape, us: 5120 x 5120 at B = 1, 2, 4,
+// 16: 7.4, 7.5, 8.2, 10.5 against 7.7 throughout; 34816 x 5120 at B = 2, 8, 16:
+// 32.1, 33.3, 35.5 against 35.7, 37.2, 39.5, and at 24 51 against 40.
+bool i8_small_wins(int64_t B, int64_t N) { return B <= 2 || (B <= 16 && N >= 8192); }
 
 hipError_t launch_i8_small(const I8Args &a, int outt, hipStream_t st)
 {
-    const bool two = a.Nh || a.RT >= 512;
-    if (a.B <= 16) {
-        if (two)
-            small_go<2, 1, 4>(a, outt, st);
-        else
-            small_go<1, 1, 5>(a, outt, st);
-    } else if (a.B <= 32) {
-        small_go<2, 2, 4>(a, outt, st);
-    } else if (a.B <= 48) {
-        small_go<2, 3, 4>(a, outt, st);
-    } else if (a.B <= 64) {
-        small_go<2, 4, 3>(a, outt, st);
-    } else {
-        small_go<2, 5, 3>(a, outt, st);
-    }
+    if (a.Nh)
+        small_go<2, 4, true>(a, outt, st);
+    else if (a.N >= 8192)
+        small_go<2, 4, false>(a, outt, st);
+    else
+        small_go<1, 5, false>(a, outt, st);
     return hipGetLastError();
 }
 

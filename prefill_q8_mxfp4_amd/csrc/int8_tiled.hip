@@ -22,8 +22,9 @@
 
 namespace qg {
 
-template <int WM_, int WN_, int TM_, int TN_>
+template <int WM_, int WN_, int TM_, int TN_, int NE_ = 0>
 struct TiShape {
+    static constexpr int NE = NE_;  // double steps of the ring, 0: the large tile's loop
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // waves, and 16-wide tiles a wave
     static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
     // KBs of a double step of codes (the same number for each wave: copies of
@@ -31,14 +32,23 @@ struct TiShape {
     static constexpr int XC = (BM / 8 + NW - 1) / NW * NW, WC = BN / 16;
     static constexpr int XPW = XC / NW, WPW = WC / NW;  // of them a wave loads
     static constexpr int XST = XC * 1024, WST = WC * 1024;
+    // LDS that a wave has to itself for its outputs, and the row groups that fit
+    static constexpr int OUT = NE ? (NW > NE ? (XST + 2 * WST) / 2 : XST + 2 * WST)
+                             : NW > 4 ? (WST < XST / 2 ? WST : XST / 2) : WST;
+    static constexpr int FIT = OUT / (TN * 1024) < 4 ? OUT / (TN * 1024) : 4, GP = FIT < TM ? FIT : TM;
+    static_assert(GP >= 1 && GP <= 4 && TM % GP == 0 && (TN == 2 || TN == 4), "whole passes of at most 64 rows");
     static_assert(XC % NW == 0 && WC % NW == 0, "whole KBs a wave");
 };
-using TiBig = TiShape<2, 4, 8, 4>;  // 256 x 256, 8 waves of 128 x 64
-using TiMid = TiShape<2, 2, 4, 4>;  // 128 x 128, 4 waves of 64 x 64
-using TiWide = TiShape<1, 4, 5, 4>;  // 80 x 256, 4 waves of 80 x 64
-using TiLow = TiShape<2, 2, 2, 4>;  // 64 x 128, 4 waves of 32 x 64
-using TiFew = TiShape<1, 4, 2, 2>;  // 32 x 128, 4 waves of 32 x 32
-using TiOne = TiShape<1, 4, 1, 2>;  // 16 x 128, 4 waves of 16 x 32
+// Rows x channels; see i8_tiled_cfg and i8_grouped_shape for which is taken when.
+using T32x32 = TiShape<2, 1, 1, 2, 8>;
+using T32x64 = TiShape<2, 2, 1, 2, 8>;
+using T64x64 = TiShape<2, 2, 2, 2, 8>;
+using T64x128 = TiShape<2, 2, 2, 4>;
+using T128x128R = TiShape<2, 4, 4, 2, 4>;
+using T128x256 = TiShape<2, 4, 4, 4>;
+using T256x256 = TiShape<2, 4, 8, 4>;
+using T32x128 = TiShape<1, 4, 2, 2>;   // routed rows only
+using T128x128 = TiShape<2, 4, 4, 2>;  // routed rows only
 
 __device__ __forceinline__ void load_chunk(__amdgpu_buffer_rsrc_t r, uint8_t *lds, int voff, int soff)
 {
@@ -61,35 +71,96 @@ __device__ __forceinline__ int ti_tile(const I8Args &a, int nt, int i)
     }
 }
 
-// Outputs of one lane for row group i: tiles j in acc (int32 sums).
+// Outputs of one lane for row group i, straight from its sums.
 template <typename S, bool DUAL, int OUTT>
 __device__ __forceinline__ void ti_store(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt, int wm,
                                          int wn, int lane, int i, const i32x4 (&acc)[S::TN])
 {
-    const int b = (wm * S::TM + i) * 16 + (lane & 15);
-    if (b >= rows)
-        return;
-    const bool vec = (a.ncols & 3) == 0;
-    const float xs = a.xs[row0 + b];
     const float *ws = (const float *)(w + a.scale_off);
     constexpr int TO = DUAL ? S::TN / 2 : S::TN;
+    const int b = (wm * S::TM + i) * 16 + (lane & 15);
+    const int n0 = (nt * S::WN + wn) * TO * 16 + (lane >> 4) * 4;
+    if (b >= rows)
+        return;
+    const float xs = a.xs[row0 + b];
+    f32x4 t[TO], tu[TO];  // all read before the first store, which a later read would wait for
 #pragma unroll
     for (int j = 0; j < TO; j++) {
-        const int n = ((nt * S::WN + wn) * TO + j) * 16 + (lane >> 4) * 4;
-        if (n >= a.ncols)
-            continue;
-        const f32x4 t = *(const f32x4 *)(ws + n);
+        const int n = n0 + j * 16 < a.ncols ? n0 + j * 16 : 0;
+        t[j] = *(const f32x4 *)(ws + n);
+        if constexpr (DUAL)
+            tu[j] = *(const f32x4 *)(ws + a.Nh + n);
+    }
+#pragma unroll
+    for (int j = 0; j < TO; j++) {
+        const int n = n0 + j * 16;
         f32x4 o;
 #pragma unroll
         for (int k = 0; k < 4; k++)
-            o[k] = (float)acc[j][k] * xs * t[k];
+            o[k] = (float)acc[j][k] * xs * t[j][k];
         if constexpr (DUAL) {
-            const f32x4 tu = *(const f32x4 *)(ws + a.Nh + n);
 #pragma unroll
             for (int k = 0; k < 4; k++)
-                o[k] = silu(o[k]) * ((float)acc[j + TO][k] * xs * tu[k]);
+                o[k] = silu(o[k]) * ((float)acc[j + TO][k] * xs * tu[j][k]);
         }
-        i8_store4<OUTT>(a.y, row0 + b, a.ncols, n, vec, o);
+        i8_put4_part<OUTT>((uint8_t *)a.y + ((row0 + b) * a.ncols + n) * (OUTT == OUT_F32 ? 4 : 2), o, a.ncols - n);
+    }
+}
+
+// A wave's outputs, GP row groups at a time through its own LDS `own`: the lanes
+// give their sums there (row by row, the 16-byte pieces of a row swizzled so that
+// neither side meets bank conflicts) and take them back a row of the tile after
+// the other, so that a store is whole cache lines and the code for it is a short
+// loop.  Straight from the accumulators the same work is some 6 KB of code, which
+// a workgroup runs once and waits for from L2: 7 to 10 us for 256 x 256 outputs.
+template <typename S, bool DUAL, int OUTT>
+__device__ __forceinline__ void ti_finish(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt,
+                                          uint8_t *own, const i32x4 (&acc)[S::TM][S::TN])
+{
+    constexpr int TO = DUAL ? S::TN / 2 : S::TN, OSZ = OUTT == OUT_F32 ? 4 : 2;
+    constexpr int PITCH = S::TN * 64, LPR = TO * 4, RPI = 64 / LPR, GR = S::GP * 16;
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wid / S::WN, wn = wid % S::WN;
+    const float *ws = (const float *)(w + a.scale_off);
+    const int c = lane % LPR, r = lane / LPR;
+    const int n = (nt * S::WN + wn) * TO * 16 + c * 4, left = a.ncols - n;
+    const int nn = left > 0 ? n : 0;  // past the last channel: the first one's, never stored
+    const f32x4 t = *(const f32x4 *)(ws + nn);
+    f32x4 tu = t;
+    if constexpr (DUAL)
+        tu = *(const f32x4 *)(ws + a.Nh + nn);
+    auto piece = [](int row, int q) { return row * PITCH + ((q ^ (S::TN == 4 ? row & 15 : (row >> 1) & 7)) << 4); };
+#pragma unroll
+    for (int p = 0; p < S::TM / S::GP; p++) {
+        const int b0 = (wm * S::TM + p * S::GP) * 16;
+        if (b0 >= rows)
+            break;  // uniform
+        const float xl = a.xs[row0 + min(b0 + (lane < GR ? lane : 0), rows - 1)];
+#pragma unroll
+        for (int i = 0; i < S::GP; i++)
+#pragma unroll
+            for (int j = 0; j < S::TN; j++)
+                *(i32x4 *)(own + piece(i * 16 + (lane & 15), j * 4 + (lane >> 4))) = acc[p * S::GP + i][j];
+        uint8_t *to = (uint8_t *)a.y + ((row0 + b0 + r) * a.ncols + n) * OSZ;
+#pragma unroll 2
+        for (int k = 0; k < GR / RPI; k++, to += (int64_t)a.ncols * RPI * OSZ) {
+            const int row = k * RPI + r;
+            const i32x4 g = *(const i32x4 *)(own + piece(row, c));
+            const float xs = __shfl(xl, row);
+            f32x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                o[e] = (float)g[e] * xs * t[e];
+            if constexpr (DUAL) {
+                const i32x4 u = *(const i32x4 *)(own + piece(row, c + LPR));
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    o[e] = silu(o[e]) * ((float)u[e] * xs * tu[e]);
+            }
+            if (b0 + row < rows)
+                i8_put4_part<OUTT>(to, o, left);
+        }
     }
 }
 
@@ -134,6 +205,49 @@ struct TiLds {
 
 __device__ __forceinline__ int x_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
+// What a wave loads of a tile: KBs of codes (rows past the last are copies of it)
+// and weight tiles; steps from `end` on come from an empty resource.
+template <typename S, bool DUAL>
+struct TiLoads {
+    const uint8_t *xbase, *wbase[S::WPW];
+    int64_t xbytes, tile_bytes;
+    int xo[S::XPW], wo, wid, end;
+
+    __device__ __forceinline__ TiLoads(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt, int end_)
+        : xbase((const uint8_t *)a.codes + row0 * a.ldc), xbytes((int64_t)rows * a.ldc),
+          tile_bytes((int64_t)a.S << 10), wo((threadIdx.x & 63) * 16),
+          wid(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), end(end_)
+    {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int c = 0; c < S::XPW; c++) {
+            const int r = (wid * S::XPW + c) * 8 + (lane >> 3);
+            xo[c] = min(r, rows - 1) * a.ldc + (((lane & 7) ^ x_swizzle(r)) << 4);
+        }
+#pragma unroll
+        for (int c = 0; c < S::WPW; c++)
+            wbase[c] = w + ti_tile<S, DUAL>(a, nt, wid * S::WPW + c) * tile_bytes;
+    }
+    // the codes of the double step kt, kt + 1
+    __device__ __forceinline__ void x(int kt, uint8_t *to) const
+    {
+        const bool live = kt < end;
+        const __amdgpu_buffer_rsrc_t xr = make_rsrc(xbase, live ? xbytes : 0);
+#pragma unroll
+        for (int c = 0; c < S::XPW; c++)
+            load_chunk(xr, to + (wid * S::XPW + c) * 1024, xo[c], live ? kt << 6 : 0);
+    }
+    // the weights of step kt
+    __device__ __forceinline__ void w(int kt, uint8_t *to) const
+    {
+        const bool live = kt < end;
+#pragma unroll
+        for (int c = 0; c < S::WPW; c++)
+            load_chunk(make_rsrc(wbase[c], live ? tile_bytes : 0), to + (wid * S::WPW + c) * 1024, wo,
+                       live ? kt << 10 : 0);
+    }
+};
+
 // One tile: rows row0 .. row0+rows-1 (at most BM), weight tile nt, steps k0 .. k1-1
 // (a multiple of 4).
 template <typename S, bool DUAL>
@@ -143,37 +257,7 @@ __device__ __forceinline__ void ti_tile_sums(const I8Args &a, const uint8_t *w, 
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wid / S::WN, wn = wid % S::WN;
-    const int64_t tile_bytes = (int64_t)a.S << 10;
-
-    // what this wave loads: KBs of codes (rows past the last are copies of it)
-    // and weight tiles
-    const uint8_t *xbase = (const uint8_t *)a.codes + row0 * a.ldc;
-    const int64_t xbytes = (int64_t)rows * a.ldc;
-    int xo[S::XPW];
-#pragma unroll
-    for (int c = 0; c < S::XPW; c++) {
-        const int r = (wid * S::XPW + c) * 8 + (lane >> 3);
-        xo[c] = min(r, rows - 1) * a.ldc + (((lane & 7) ^ x_swizzle(r)) << 4);
-    }
-    const uint8_t *wbase[S::WPW];
-#pragma unroll
-    for (int c = 0; c < S::WPW; c++)
-        wbase[c] = w + ti_tile<S, DUAL>(a, nt, wid * S::WPW + c) * tile_bytes;
-
-    auto load_x = [&](int kt, uint8_t *to) {  // the double step kt, kt + 1
-        const bool live = kt < k1;
-        const __amdgpu_buffer_rsrc_t xr = make_rsrc(xbase, live ? xbytes : 0);
-#pragma unroll
-        for (int c = 0; c < S::XPW; c++)
-            load_chunk(xr, to + (wid * S::XPW + c) * 1024, xo[c], live ? kt << 6 : 0);
-    };
-    auto load_w = [&](int kt, uint8_t *to) {
-        const bool live = kt < k1;
-#pragma unroll
-        for (int c = 0; c < S::WPW; c++)
-            load_chunk(make_rsrc(wbase[c], live ? tile_bytes : 0), to + (wid * S::WPW + c) * 1024, lane * 16,
-                       live ? kt << 10 : 0);
-    };
+    const TiLoads<S, DUAL> ld(a, w, row0, rows, nt, k1);
     i32x4 xf[2][S::TM], wf[2][S::TN];
     // row r = lane % 16 of a group of 16 and its k group, in the even step; the
     // odd step's piece is 4 further on, which the swizzle leaves a flip of one bit
@@ -194,12 +278,12 @@ __device__ __forceinline__ void ti_tile_sums(const I8Args &a, const uint8_t *w, 
         for (int j = 0; j < S::TN; j++)
             acc[i][j] = i32x4{0, 0, 0, 0};
     // in the order that the loop keeps: a step's weights, then (odd steps) codes
-    load_x(k0, lds.x[0]);
-    load_w(k0, lds.w[0]);
-    load_w(k0 + 1, lds.w[1]);
-    load_x(k0 + 2, lds.x[1]);
-    load_w(k0 + 2, lds.w[2]);
-    load_w(k0 + 3, lds.w[3]);
+    ld.x(k0, lds.x[0]);
+    ld.w(k0, lds.w[0]);
+    ld.w(k0 + 1, lds.w[1]);
+    ld.x(k0 + 2, lds.x[1]);
+    ld.w(k0 + 2, lds.w[2]);
+    ld.w(k0 + 3, lds.w[3]);
     step_barrier<S::XPW + 3 * S::WPW>();
     read(lds.x[0], lds.w[0], 0, 0);
     for (int kt = k0; kt < k1; kt += 4) {
@@ -212,9 +296,9 @@ __device__ __forceinline__ void ti_tile_sums(const I8Args &a, const uint8_t *w, 
                 step_barrier<S::WPW>();
             else
                 step_barrier<S::XPW + 2 * S::WPW>();
-            load_w(kt + u + 4, lds.w[u]);
+            ld.w(kt + u + 4, lds.w[u]);
             if (u & 1)
-                load_x(kt + u + 3, lds.x[u / 2]);
+                ld.x(kt + u + 3, lds.x[u / 2]);
             read(lds.x[(u + 1) / 2 % 2], lds.w[(u + 1) % 4], (u + 1) & 1, (u + 1) & 1);
 #pragma unroll
             for (int i = 0; i < S::TM; i++)
@@ -227,8 +311,105 @@ __device__ __forceinline__ void ti_tile_sums(const I8Args &a, const uint8_t *w, 
                 ti_interleave<S::WPW, S::TM + S::TN, S::TM * S::TN>();
         }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load outlives the workgroup's LDS
+    step_barrier<0>();  // no load outlives this, and every wave is done with the stages
 }
+
+// The same sums for small tiles, whose steps take less time than a barrier and an
+// LDS read: a ring of NE double steps, all but one of them in flight, one barrier
+// a double step.
+template <typename S, bool DUAL, int NE>
+__device__ __forceinline__ void ti_deep_sums(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt, int k0,
+                                             int k1, uint8_t *const (&ring)[NE], i32x4 (&acc)[S::TM][S::TN])
+{
+    constexpr int LPE = S::XPW + 2 * S::WPW;  // loads a wave issues each double step
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wid / S::WN, wn = wid % S::WN;
+    const TiLoads<S, DUAL> ld(a, w, row0, rows, nt, k1);
+    auto load = [&](int kt, uint8_t *to) {
+        ld.x(kt, to);
+        ld.w(kt, to + S::XST);
+        ld.w(kt + 1, to + S::XST + S::WST);
+    };
+    const int r16 = lane & 15;
+    const int xl = wm * S::TM * 2048 + r16 * 128 + (((lane >> 4) ^ x_swizzle(r16)) << 4);
+    const int wl = S::XST + wn * S::TN * 1024 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < S::TM; i++)
+#pragma unroll
+        for (int j = 0; j < S::TN; j++)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < NE - 1; u++)
+        load(k0 + 2 * u, ring[u]);
+    auto step = [&](int kt, int u) {  // double step kt, in ring[u]
+        step_barrier<LPE *(NE - 2)>();
+        load(kt + 2 * (NE - 1), ring[(u + NE - 1) % NE]);
+        const uint8_t *at = ring[u];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            i32x4 xf[S::TM], wf[S::TN];
+#pragma unroll
+            for (int j = 0; j < S::TN; j++)
+                wf[j] = *(const i32x4 *)(at + wl + h * S::WST + j * 1024);
+#pragma unroll
+            for (int i = 0; i < S::TM; i++)
+                xf[i] = *(const i32x4 *)(at + (xl ^ (h << 6)) + i * 2048);
+#pragma unroll
+            for (int i = 0; i < S::TM; i++)
+#pragma unroll
+                for (int j = 0; j < S::TN; j++)
+                    acc[i][j] = mfma_i8(wf[j], xf[i], acc[i][j]);
+        }
+    };
+    int kt = k0;
+    for (; kt + 2 * NE <= k1; kt += 2 * NE) {
+#pragma unroll
+        for (int u = 0; u < NE; u++)
+            step(kt + 2 * u, u);
+    }
+    // the rest, in pairs of double steps
+#pragma unroll
+    for (int u = 0; u < NE - 2; u += 2) {
+        if (kt + 2 * u < k1) {  // uniform
+            step(kt + 2 * u, u);
+            step(kt + 2 * u + 2, u + 1);
+        }
+    }
+    step_barrier<0>();  // no load outlives this, and every wave is done with the stages
+}
+
+// A wave's own LDS once the stages are done with.
+template <typename S>
+__device__ __forceinline__ uint8_t *ti_own(const TiLds &l, int wid)
+{
+    if (wid < 4)
+        return wid == 0 ? l.w[0] : wid == 1 ? l.w[1] : wid == 2 ? l.w[2] : l.w[3];
+    return (wid < 6 ? l.x[0] : l.x[1]) + (wid & 1) * (S::XST / 2);
+}
+
+// The sums of one tile in the way its shape has them, and the wave's own LDS after.
+#define TI_SUMS(S, DUAL, ...)                                                                                       \
+    uint8_t *own;                                                                                                   \
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);                                              \
+    if constexpr (S::NE == 0) {                                                                                     \
+        TI_LDS(S, lds);                                                                                             \
+        ti_tile_sums<S, DUAL>(__VA_ARGS__, lds, acc);                                                               \
+        own = ti_own<S>(lds, wave);                                                                                 \
+    } else {                                                                                                        \
+        constexpr int RB = S::XST + 2 * S::WST, R8 = S::NE > 4 ? RB : 16;                                           \
+        __shared__ __attribute__((aligned(1024))) uint8_t r0[RB], r1[RB], r2[RB], r3[RB];                           \
+        __shared__ __attribute__((aligned(1024))) uint8_t r4[R8], r5[R8], r6[R8], r7[R8];                           \
+        if constexpr (S::NE == 4) {                                                                                 \
+            uint8_t *const ring[4] = {r0, r1, r2, r3};                                                              \
+            ti_deep_sums<S, DUAL, 4>(__VA_ARGS__, ring, acc);                                                       \
+        } else {                                                                                                    \
+            uint8_t *const ring[8] = {r0, r1, r2, r3, r4, r5, r6, r7};                                              \
+            ti_deep_sums<S, DUAL, 8>(__VA_ARGS__, ring, acc);                                                       \
+        }                                                                                                           \
+        const int at = S::NW > S::NE ? wave / 2 : wave;                                                             \
+        own = (at == 0 ? r0 : at == 1 ? r1 : at == 2 ? r2 : r3) + (S::NW > S::NE ? (wave & 1) * (RB / 2) : 0);      \
+    }
 
 // Workgroup id -> tile: consecutive ids go to the 8 XCDs in turn, so an XCD's
 // share is made one run of tiles, batch tiles fastest: the tiles an XCD works
@@ -240,11 +421,43 @@ __device__ __forceinline__ int xcd_order(int id, int n)
     return xcd < full ? xcd * per + loc : full * per + (xcd - full) * (per - 1) + loc;
 }
 
+// One whole tile of shape S in LDS made for a shape at least as large.
+template <typename S, bool DUAL, int OUTT>
+__device__ __forceinline__ void ti_whole(const I8Args &a, int mt, int nt, const TiLds &lds)
+{
+    const int64_t row0 = (int64_t)mt * S::BM;
+    const int rows = min(S::BM, (int)(a.B - row0));
+    if (rows <= 0 || nt * (S::BN / (DUAL ? 2 : 1)) >= a.ncols)
+        return;  // uniform: a piece of a tile that lies outside
+    i32x4 acc[S::TM][S::TN];
+    ti_tile_sums<S, DUAL>(a, a.w, row0, rows, nt, 0, a.S, lds, acc);
+    ti_finish<S, DUAL, OUTT>(a, a.w, row0, rows, nt,
+                             ti_own<S>(lds, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), acc);
+}
+
+// 256 x 256 tiles: the first `full` whole, the others as PIECES (1, 2 or 4)
+// smaller ones each.  Whole rounds of 256 tiles run first; a last, partial round
+// of whole tiles would leave most of the chip idle for a tile's time, its pieces
+// share it out.
+template <int PIECES, bool DUAL, int OUTT>
+__global__ __launch_bounds__(512, 2) void i8_big_kernel(I8Args a, int mtiles, int ntiles, int full)
+{
+    TI_LDS(T256x256, lds);
+    using P = TiShape<2, 4, PIECES == 1 ? 8 : 4, PIECES == 4 ? 2 : 4>;
+    constexpr int PM = T256x256::BM / P::BM, PN = T256x256::BN / P::BN;
+    if (blockIdx.x < full) {
+        const int t = xcd_order(blockIdx.x, full);
+        ti_whole<T256x256, DUAL, OUTT>(a, t % mtiles, t / mtiles, lds);
+    } else {
+        const int t = xcd_order(blockIdx.x - full, gridDim.x - full), tile = full + t / PIECES, p = t % PIECES;
+        ti_whole<P, DUAL, OUTT>(a, tile % mtiles * PM + p % PM, tile / mtiles * PN + p / PM, lds);
+    }
+}
+
 template <typename S, bool DUAL, int OUTT>
 __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int mtiles, int ntiles,
                                                                                 int split, int32_t *part)
 {
-    TI_LDS(S, lds);
     const int t = xcd_order(blockIdx.x, gridDim.x);
     const int tile = t / split, piece = t % split;
     const int mt = tile % mtiles, nt = tile / mtiles;
@@ -253,7 +466,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int m
     const int64_t row0 = (int64_t)mt * S::BM;
     const int rows = min(S::BM, (int)(a.B - row0));
     i32x4 acc[S::TM][S::TN];
-    ti_tile_sums<S, DUAL>(a, a.w, row0, rows, nt, k0, k1, lds, acc);
+    TI_SUMS(S, DUAL, a, a.w, row0, rows, nt, k0, k1)
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     if (split > 1) {
         i32x4 *p = (i32x4 *)part + ((int64_t)t * S::NW + wid) * S::TM * S::TN * 64;
@@ -264,9 +477,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int m
                 p[(i * S::TN + j) * 64 + lane] = acc[i][j];
         return;
     }
-#pragma unroll
-    for (int i = 0; i < S::TM; i++)
-        ti_store<S, DUAL, OUTT>(a, a.w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc[i]);
+    ti_finish<S, DUAL, OUTT>(a, a.w, row0, rows, nt, own, acc);
 }
 
 // The split's partial tiles, a wave a row group of a wave's part of a tile.
@@ -279,19 +490,19 @@ __global__ __launch_bounds__(64) void i8_tiled_reduce_kernel(I8Args a, int mtile
     const int mt = tile % mtiles, nt = tile / mtiles;
     const int64_t row0 = (int64_t)mt * S::BM;
     const int rows = min(S::BM, (int)(a.B - row0));
-    i32x4 acc[S::TN];
+    i32x4 acc[1][S::TN];
 #pragma unroll
     for (int j = 0; j < S::TN; j++)
-        acc[j] = i32x4{0, 0, 0, 0};
+        acc[0][j] = i32x4{0, 0, 0, 0};
     if ((wid / S::WN * S::TM + i) * 16 >= rows)
         return;
     for (int p = 0; p < split; p++) {
         const i32x4 *q = (const i32x4 *)part + (((int64_t)tile * split + p) * S::NW + wid) * S::TM * S::TN * 64;
 #pragma unroll
         for (int j = 0; j < S::TN; j++)
-            acc[j] += q[(i * S::TN + j) * 64 + lane];
+            acc[0][j] += q[(i * S::TN + j) * 64 + lane];
     }
-    ti_store<S, DUAL, OUTT>(a, a.w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc);
+    ti_store<S, DUAL, OUTT>(a, a.w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc[0]);
 }
 
 // Rows sorted by expert: the grid covers a bound on the experts' row tiles, each
@@ -300,9 +511,8 @@ __global__ __launch_bounds__(64) void i8_tiled_reduce_kernel(I8Args a, int mtile
 // the XCDs in turn (the real ones are the first of the bound, so runs of them
 // would leave half of the XCDs idle), a row tile's weight tiles to one XCD.
 template <typename S, bool DUAL, int OUTT>
-__global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args a, I8Groups grp, int ntiles)
+__global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8Groups grp, int ntiles)
 {
-    TI_LDS(S, lds);
     __shared__ int wsum[S::NW], found[4];
     constexpr int NT = 64 * S::NW;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
@@ -365,38 +575,91 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_grouped_kernel(I8Args 
     const int rows = min(S::BM, __builtin_amdgcn_readfirstlane(found[2]) - row0);
     const uint8_t *w = uniform_ptr(grp.wtab[e]);
     i32x4 acc[S::TM][S::TN];
-    ti_tile_sums<S, DUAL>(a, w, row0, rows, nt, 0, a.S, lds, acc);
-#pragma unroll
-    for (int i = 0; i < S::TM; i++)
-        ti_store<S, DUAL, OUTT>(a, w, row0, rows, nt, wid / S::WN, wid % S::WN, lane, i, acc[i]);
+    TI_SUMS(S, DUAL, a, w, row0, rows, nt, 0, a.S)
+    ti_finish<S, DUAL, OUTT>(a, w, row0, rows, nt, own, acc);
 }
 
 // ------------------------------------------------------------------ host
 
-// Whole tiles of the larger shape when they fill the chip, else the smaller
-// one, K split so that at least a round of tiles runs.
-I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int bm, int forced)
+// What a call costs with a shape, in us, fitted to times on MI355X (K = 256 to
+// 17408; 5 to 35000 channels, 1 to 4096 rows; within 10 % of nearly all of them).
+// A workgroup takes `fixed` for its first loads and its outputs and a step's time
+// for each 64 k; that time grows with the workgroups at work, for their share of
+// L2 and of the clock: step[0] with up to 128 of them, step[1] with 256, step[2]
+// with all that the CUs hold.  Choices it makes, with the runner-up: 16 x 5120 x
+// 5120 32x32 7.8 (32x64 8.5); 70 x 5120 x 17408 32x64 28 (64x64 31); 128 x 5120 x
+// 5120 64x64 11.7 (32x64 15.7); 512 x 5120 x 5120 128x128R 21 (64x128 24); 1024:
+// 128x256 32 (64x128 39); 2048: 256x256 55 (128x128R 66).
+struct ShapeCost {
+    int BM, BN, resident;  // workgroups a CU holds
+    float fixed, step[3];
+};
+static const ShapeCost COST[] = {
+    {0, 0, 0, 0.f, {0.f, 0.f, 0.f}},
+    {32, 32, 2, 1.0f, {0.067f, 0.075f, 0.110f}},    // I8_32x32
+    {32, 64, 1, 0.3f, {0.085f, 0.092f, 0.092f}},    // I8_32x64
+    {64, 64, 1, 0.8f, {0.103f, 0.112f, 0.112f}},    // I8_64x64
+    {64, 128, 3, 1.0f, {0.225f, 0.250f, 0.520f}},   // I8_64x128
+    {128, 128, 1, 1.0f, {0.200f, 0.280f, 0.280f}},  // I8_128x128R
+    {128, 256, 1, 2.0f, {0.300f, 0.520f, 0.520f}},  // I8_128x256
+    {256, 256, 1, 5.0f, {0.540f, 0.820f, 0.820f}},  // I8_256x256
+};
+
+// One round of n workgroups (n <= 256 * resident) of `steps` steps.
+static float round_us(const ShapeCost &p, int64_t n, int steps)
 {
-    I8TiCfg c;
-    const int cols = a.Nh ? 2 * a.Nh : a.N;
-    const int64_t big = (int64_t)((a.B + 255) / 256) * ((cols + 255) / 256);
-    c.BM = bm ? bm : big >= 192 ? 256 : 128;
-    c.BN = c.BM == 80 || c.BM == 256 ? 256 : 128;
-    c.mtiles = (a.B + c.BM - 1) / c.BM;
-    c.ntiles = (cols + c.BN - 1) / c.BN;
-    const int64_t tiles = (int64_t)c.mtiles * c.ntiles;
-    const int steps = a.S / 4;  // in fours, as the kernel walks them
-    c.split = 1;
-    if (split && tiles < 256) {
-        int s = (int)(512 / tiles);
-        s = s > steps / 2 ? steps / 2 : s;
-        s = s < 1 ? 1 : s;
-        if (forced) s = forced > steps ? steps : forced;
-        const int per = (steps + s - 1) / s;
-        c.split = (steps + per - 1) / per;  // no empty piece
+    float t = p.step[0];
+    if (n > 256)
+        t = p.step[1] + (p.step[2] - p.step[1]) * (float)(n - 256) / (256.f * (p.resident - 1));
+    else if (n > 128)
+        t += (p.step[1] - t) * (float)(n - 128) / 128.f;
+    return p.fixed + t * steps;
+}
+
+// Pieces of each 256 x 256 tile of the last, partial round: as many as still fit
+// one round.
+static int big_pieces(int64_t tiles)
+{
+    const int64_t rem = tiles % 256;
+    return tiles < 256 || rem == 0 || rem > 128 ? 1 : rem > 64 ? 2 : 4;
+}
+
+I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int shape, int pieces)
+{
+    const int cols = a.Nh ? 2 * a.Nh : a.N, fours = a.S / 4;
+    I8TiCfg best = {};
+    float best_us = 1e30f;
+    for (int k = I8_32x32; k <= I8_256x256; k++) {
+        if (shape >= I8_32x32 && shape <= I8_256x256 && k != shape)
+            continue;
+        const ShapeCost &p = COST[k];
+        I8TiCfg c;
+        c.shape = k;
+        c.mtiles = (a.B + p.BM - 1) / p.BM;
+        c.ntiles = (cols + p.BN - 1) / p.BN;
+        const int64_t tiles = (int64_t)c.mtiles * c.ntiles;
+        for (int s = 1; s <= 16 && s <= fours; s *= 2) {
+            if (s > 1 && (!split || tiles >= 256))
+                break;  // enough workgroups as it is
+            const int want = split && pieces ? (pieces < fours ? pieces : fours) : s;
+            const int per = (fours + want - 1) / want;
+            c.split = (fours + per - 1) / per;  // no empty piece
+            c.part_bytes = c.split > 1 ? tiles * c.split * p.BM * p.BN * 4 : 0;
+            const int64_t wgs = tiles * c.split, round = 256 * p.resident, rest = wgs % round;
+            float us = (float)(wgs / round) * round_us(p, round, 4 * per);
+            if (rest && k == I8_256x256 && c.split == 1 && big_pieces(tiles) > 1)
+                us += round_us(COST[big_pieces(tiles) == 4 ? I8_128x128R : I8_128x256], rest * big_pieces(tiles), 4 * per);
+            else if (rest)
+                us += round_us(p, rest, 4 * per);
+            if (c.split > 1)  // a second launch, and the partial tiles written and read
+                us += 3.f + 0.5e-6f * (float)c.part_bytes;
+            if (us < best_us) {
+                best_us = us;
+                best = c;
+            }
+        }
     }
-    c.part_bytes = c.split > 1 ? tiles * c.split * c.BM * c.BN * 4 : 0;
-    return c;
+    return best;
 }
 
 template <typename S, bool DUAL, int OUTT>
@@ -410,28 +673,48 @@ static void tiled_go(const I8Args &a, const I8TiCfg &c, int32_t *part, hipStream
                            0, st, a, c.mtiles, c.split, part);
 }
 
-template <typename S>
-static void tiled_shape(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st)
+template <bool DUAL, int OUTT>
+static void big_go(const I8Args &a, const I8TiCfg &c, hipStream_t st)
 {
-    if (a.Nh && outt == OUT_F32)
-        tiled_go<S, true, OUT_F32>(a, c, part, st);
-    else if (a.Nh)
-        tiled_go<S, true, OUT_BF16>(a, c, part, st);
-    else if (outt == OUT_F32)
-        tiled_go<S, false, OUT_F32>(a, c, part, st);
+    const int tiles = c.mtiles * c.ntiles, pieces = big_pieces(tiles);
+    const int full = pieces == 1 ? tiles : tiles / 256 * 256;
+    const dim3 grid((unsigned)(full + (tiles - full) * pieces)), blk(512);
+    if (pieces == 4)
+        hipLaunchKernelGGL((i8_big_kernel<4, DUAL, OUTT>), grid, blk, 0, st, a, c.mtiles, c.ntiles, full);
+    else if (pieces == 2)
+        hipLaunchKernelGGL((i8_big_kernel<2, DUAL, OUTT>), grid, blk, 0, st, a, c.mtiles, c.ntiles, full);
     else
-        tiled_go<S, false, OUT_BF16>(a, c, part, st);
+        hipLaunchKernelGGL((i8_big_kernel<1, DUAL, OUTT>), grid, blk, 0, st, a, c.mtiles, c.ntiles, full);
+}
+
+template <bool DUAL, int OUTT>
+static void tiled_shape(const I8Args &a, const I8TiCfg &c, int32_t *part, hipStream_t st)
+{
+    switch (c.shape) {
+    case I8_32x32: tiled_go<T32x32, DUAL, OUTT>(a, c, part, st); break;
+    case I8_32x64: tiled_go<T32x64, DUAL, OUTT>(a, c, part, st); break;
+    case I8_64x64: tiled_go<T64x64, DUAL, OUTT>(a, c, part, st); break;
+    case I8_64x128: tiled_go<T64x128, DUAL, OUTT>(a, c, part, st); break;
+    case I8_128x128R: tiled_go<T128x128R, DUAL, OUTT>(a, c, part, st); break;
+    case I8_128x256: tiled_go<T128x256, DUAL, OUTT>(a, c, part, st); break;
+    default:
+        if (c.split > 1)
+            tiled_go<T256x256, DUAL, OUTT>(a, c, part, st);
+        else
+            big_go<DUAL, OUTT>(a, c, st);
+    }
 }
 
 hipError_t launch_i8_tiled(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st)
 {
-    switch (c.BM) {
-    case 32: tiled_shape<TiFew>(a, c, part, outt, st); break;
-    case 64: tiled_shape<TiLow>(a, c, part, outt, st); break;
-    case 80: tiled_shape<TiWide>(a, c, part, outt, st); break;
-    case 128: tiled_shape<TiMid>(a, c, part, outt, st); break;
-    default: tiled_shape<TiBig>(a, c, part, outt, st); break;
-    }
+    if (a.Nh && outt == OUT_F32)
+        tiled_shape<true, OUT_F32>(a, c, part, st);
+    else if (a.Nh)
+        tiled_shape<true, OUT_BF16>(a, c, part, st);
+    else if (outt == OUT_F32)
+        tiled_shape<false, OUT_F32>(a, c, part, st);
+    else
+        tiled_shape<false, OUT_BF16>(a, c, part, st);
     return hipGetLastError();
 }
 
@@ -444,22 +727,32 @@ static void grouped_go(const I8Args &a, const I8Groups &g, int outt, hipStream_t
     const int64_t tiles = a.B / S::BM + (g.E < a.B ? g.E : a.B);
     const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * ntiles)), blk(64 * S::NW);
     if (a.Nh && outt == OUT_F32)
-        hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, true, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
     else if (a.Nh)
-        hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, true, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
     else if (outt == OUT_F32)
-        hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, false, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
     else
-        hipLaunchKernelGGL((i8_tiled_grouped_kernel<S, false, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
 }
 
-hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int bm, int outt, hipStream_t st)
+// Rows of a tile by the mean rows of an expert.  Measured with 128 experts of
+// 1024 x 2048, rows dealt evenly and unevenly, us for 32 / 64 / 128 rows a tile:
+// mean 8: 57 / 57 / 54 and 55 / 55 / 51; 24: 61 / 62 / 58 and 63 / 61 / 63;
+// 48: 93 / 64 / 61 and 88 / 69 / 71; 96: 128 / 98 / 70 and 130 / 97 / 83; of
+// 2048 x 512: mean 8: 33 / 35 / 39 and 32 / 35 / 38; 24: 37 / 40 / 43 and
+// 43 / 40 / 45; 48: 60 / 43 / 48 and 62 / 50 / 52; 96: 93 / 74 / 60 and 90 / 74 / 69.
+int i8_grouped_shape(int64_t E, int64_t T)
 {
-    switch (bm) {
-    case 16: grouped_go<TiOne>(a, g, outt, st); break;
-    case 32: grouped_go<TiFew>(a, g, outt, st); break;
-    case 64: grouped_go<TiLow>(a, g, outt, st); break;
-    default: grouped_go<TiMid>(a, g, outt, st); break;
+    return T < 16 * E ? I8_32x128 : T < 36 * E ? I8_64x128 : I8_128x128;
+}
+
+hipError_t launch_i8_grouped(const I8Args &a, const I8Groups &g, int shape, int outt, hipStream_t st)
+{
+    switch (shape) {
+    case I8_32x128: grouped_go<T32x128>(a, g, outt, st); break;
+    case I8_64x128: grouped_go<T64x128>(a, g, outt, st); break;
+    default: grouped_go<T128x128>(a, g, outt, st); break;
     }
     return hipGetLastError();
 }

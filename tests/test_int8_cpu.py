@@ -74,7 +74,7 @@ def test_tiers():
     p = q.Plan("int8", 5120, 5120, act="bf16")
     assert p.math == "int8"
     assert p.tier(1) == "skinny" and p.tier(4096) == "tiled"
-    assert p.grouped_tier(512, 160) == "skinny" and p.grouped_tier(4, 4096) == "tiled"
+    assert p.grouped_tier(512, 160) == "tiled" and p.grouped_tier(4, 4096) == "tiled"
     assert q.Plan("int8", 64, 64, tier="tiled").tier(1) == "tiled"
     assert q.Plan("int8", 64, 64, tier="tiled").grouped_tier(8, 8) == "tiled"
     assert q.Plan("int8", 64, 64, tier="skinny").tier(4096) == "skinny"

@@ -160,6 +160,45 @@ def test_product(B, N, K, out):
             assert torch.equal(y, first), (tier, ws)
 
 
+@pytest.mark.parametrize("shape", range(1, 8))
+@pytest.mark.parametrize("B,N,K", [(5, 70, 200), (130, 300, 700), (300, 544, 2100)])
+def test_product_tile_shapes(B, N, K, shape, monkeypatch):
+    """Every tile shape of the large-batch tier, its K in one, two and five
+    pieces, plain and fused: the same bits as the small-batch tier."""
+    g = gen(B + shape)
+    _, _, dx, dsx = code_rows(B, K, g)
+    cw, sw, packed = weight(N, K, g)
+    for epi, n in (("none", N), ("swiglu", N // 32 * 32)):
+        w = packed if epi == "none" else q.pack_int8(cw[:n].contiguous().to(DEV), sw[:n].contiguous().to(DEV))
+        cols = n if epi == "none" else n // 2
+        monkeypatch.delenv("QGEMM_I8_SHAPE", raising=False)
+        monkeypatch.delenv("QGEMM_TI_SPLIT", raising=False)
+        small = q.Plan("int8", n, K, act="bf16", out="f32", epilogue=epi, tier="skinny")
+        want = small.run_codes(dx, dsx, w, torch.empty(B, cols, device=DEV))
+        monkeypatch.setenv("QGEMM_I8_SHAPE", str(shape))
+        for pieces in (1, 2, 5):
+            monkeypatch.setenv("QGEMM_TI_SPLIT", str(pieces))
+            plan = q.Plan("int8", n, K, act="bf16", out="f32", epilogue=epi, tier="tiled")
+            y = plan.run_codes(dx, dsx, w, torch.full((B, cols), float("nan"), device=DEV))
+            assert torch.equal(y, want), (epi, pieces)
+
+
+@pytest.mark.parametrize("B,N,K,swiglu", [(520, 25 * 256 * 4 + 40, 96, False), (1030, 2 * 128 * 90, 80, True),
+                                          (300, 160 * 256, 64, False)])
+def test_product_last_round_in_pieces(B, N, K, swiglu, monkeypatch):
+    """More 256 x 256 tiles than a round: the last round's cut in 4, 1 and 2."""
+    g = gen(B)
+    _, _, dx, dsx = code_rows(B, K, g)
+    cw = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int64).to(torch.int8).to(DEV)
+    w = q.pack_int8(cw, torch.rand(N, generator=g).to(DEV))
+    epi, cols = ("swiglu", N // 2) if swiglu else ("none", N)
+    monkeypatch.setenv("QGEMM_I8_SHAPE", "7")
+    ys = [q.Plan("int8", N, K, act="bf16", out="bf16", epilogue=epi, tier=t).run_codes(
+        dx, dsx, w, torch.full((B, cols), float("nan"), dtype=torch.bfloat16, device=DEV))
+        for t in ("skinny", "tiled")]
+    assert torch.equal(*ys)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("B,nh,K", [(1, 16, 64), (3, 48, 131), (16, 272, 512), (40, 80, 1000), (70, 144, 2729),
                                     (200, 528, 640), (513, 160, 256)])
@@ -251,8 +290,8 @@ def experts(E, N, K, g):
     ([1], 16 * 2, 64, 0), ([0, 3, 0, 0, 17, 1, 0], 96, 131, 5), ([64, 65, 0, 16, 33], 160, 640, 0),
     ([0, 0, 0], 64, 64, 4), ([200, 0, 129, 128, 1, 300], 288, 333, 70), ([5] * 70, 64, 200, 1),
     ([1000], 96, 100, 0)])
-def test_experts(counts, N, K, behind, swiglu):
-    """Each expert's rows are those of a dense call, on both routes; rows
+def test_experts(counts, N, K, behind, swiglu, monkeypatch):
+    """Each expert's rows are those of a dense call, for each tile shape; rows
     behind the last expert's are neither read (they would be NaN) nor written."""
     E, T = len(counts), sum(counts) + behind
     g = gen(T + N)
@@ -262,8 +301,11 @@ def test_experts(counts, N, K, behind, swiglu):
     off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
     epi, ncols = ("swiglu", N // 2) if swiglu else ("none", N)
     for out in ("f32", "bf16"):
-        for tier in (None, "skinny", "tiled"):
-            plan = q.Plan("int8", N, K, act="bf16", out=out, epilogue=epi, tier=tier)
+        for tier in (None, 4, 8, 9):      # by the mean count, and each of its tile shapes
+            if tier is not None:
+                monkeypatch.setenv("QGEMM_I8_SHAPE", str(tier))
+            plan = q.Plan("int8", N, K, act="bf16", out=out, epilogue=epi)
+            monkeypatch.delenv("QGEMM_I8_SHAPE", raising=False)
             y = torch.full((T, ncols), 7.0, dtype=DT[out], device=DEV)
             plan.run_grouped_codes(dx, dsx, table, off, y)
             assert (y[T - behind:] == 7.0).all()
@@ -280,14 +322,15 @@ def test_experts(counts, N, K, behind, swiglu):
     assert q.device_status() & q.DEV_BAD_OFFSETS == 0
 
 
-@pytest.mark.parametrize("tier", ["skinny", "tiled"])
-def test_experts_bad_offsets(tier):
+@pytest.mark.parametrize("shape", [4, 8, 9])
+def test_experts_bad_offsets(shape, monkeypatch):
     """An expert whose offsets break the rules is left out and reported."""
     N, K, T, E = 64, 128, 40, 4
     g = gen(1)
     _, _, dx, dsx = code_rows(T, K, g)
     _, table = experts(E, N, K, g)
-    plan = q.Plan("int8", N, K, act="bf16", out="f32", tier=tier)
+    monkeypatch.setenv("QGEMM_I8_SHAPE", str(shape))
+    plan = q.Plan("int8", N, K, act="bf16", out="f32")
     q.device_status(clear=True)
     for off in ([0, 10, 5, 20, 40], [0, 10, 20, 30, 41], [1, 10, 20, 30, 40], [0, -1, 20, 30, 40],
                 [0, 10, 2 ** 31 - 1, 30, 40]):
