@@ -107,6 +107,28 @@ __device__ __forceinline__ void ti_store(const I8Args &a, const uint8_t *w, int6
     }
 }
 
+// The scales of a wave's outputs: of its lane's four channels (the same in every
+// pass) and of the rows of each pass, a row a lane.  Read before the sums, so that
+// no read waits behind a store.
+template <typename S, bool DUAL>
+struct TiScales {
+    static constexpr int TO = DUAL ? S::TN / 2 : S::TN, LPR = TO * 4, GR = S::GP * 16;
+    f32x4 t, tu;
+    float xs[S::TM / S::GP];
+    __device__ __forceinline__ TiScales(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt)
+    {
+        const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+        const int n = (nt * S::WN + wid % S::WN) * TO * 16 + lane % LPR * 4;
+        const float *ws = (const float *)(w + a.scale_off) + (n < a.ncols ? n : 0);
+        t = tu = *(const f32x4 *)ws;
+        if constexpr (DUAL)
+            tu = *(const f32x4 *)(ws + a.Nh);
+#pragma unroll
+        for (int p = 0; p < S::TM / S::GP; p++)
+            xs[p] = a.xs[row0 + min((wid / S::WN * S::TM + p * S::GP) * 16 + (lane < GR ? lane : 0), rows - 1)];
+    }
+};
+
 // A wave's outputs, GP row groups at a time through its own LDS `own`: the lanes
 // give their sums there (row by row, the 16-byte pieces of a row swizzled so that
 // neither side meets bank conflicts) and take them back a row of the tile after
@@ -114,7 +136,7 @@ __device__ __forceinline__ void ti_store(const I8Args &a, const uint8_t *w, int6
 // loop.  Straight from the accumulators the same work is some 6 KB of code, which
 // a workgroup runs once and waits for from L2: 7 to 10 us for 256 x 256 outputs.
 template <typename S, bool DUAL, int OUTT>
-__device__ __forceinline__ void ti_finish(const I8Args &a, const uint8_t *w, int64_t row0, int rows, int nt,
+__device__ __forceinline__ void ti_finish(const I8Args &a, const TiScales<S, DUAL> &sc, int64_t row0, int rows, int nt,
                                           uint8_t *own, const i32x4 (&acc)[S::TM][S::TN])
 {
     constexpr int TO = DUAL ? S::TN / 2 : S::TN, OSZ = OUTT == OUT_F32 ? 4 : 2;
@@ -122,32 +144,25 @@ __device__ __forceinline__ void ti_finish(const I8Args &a, const uint8_t *w, int
     const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wid / S::WN, wn = wid % S::WN;
-    const float *ws = (const float *)(w + a.scale_off);
     const int c = lane % LPR, r = lane / LPR;
     const int n = (nt * S::WN + wn) * TO * 16 + c * 4, left = a.ncols - n;
-    const int nn = left > 0 ? n : 0;  // past the last channel: the first one's, never stored
-    const f32x4 t = *(const f32x4 *)(ws + nn);
-    f32x4 tu = t;
-    if constexpr (DUAL)
-        tu = *(const f32x4 *)(ws + a.Nh + nn);
+    const f32x4 t = sc.t, tu = sc.tu;
     auto piece = [](int row, int q) { return row * PITCH + ((q ^ (S::TN == 4 ? row & 15 : (row >> 1) & 7)) << 4); };
 #pragma unroll
     for (int p = 0; p < S::TM / S::GP; p++) {
         const int b0 = (wm * S::TM + p * S::GP) * 16;
         if (b0 >= rows)
             break;  // uniform
-        const float xl = a.xs[row0 + min(b0 + (lane < GR ? lane : 0), rows - 1)];
 #pragma unroll
         for (int i = 0; i < S::GP; i++)
 #pragma unroll
             for (int j = 0; j < S::TN; j++)
                 *(i32x4 *)(own + piece(i * 16 + (lane & 15), j * 4 + (lane >> 4))) = acc[p * S::GP + i][j];
         uint8_t *to = (uint8_t *)a.y + ((row0 + b0 + r) * a.ncols + n) * OSZ;
-#pragma unroll 2
-        for (int k = 0; k < GR / RPI; k++, to += (int64_t)a.ncols * RPI * OSZ) {
-            const int row = k * RPI + r;
+        const int64_t next = (int64_t)a.ncols * RPI * OSZ;
+        auto out = [&](int row) {
             const i32x4 g = *(const i32x4 *)(own + piece(row, c));
-            const float xs = __shfl(xl, row);
+            const float xs = __shfl(sc.xs[p], row);
             f32x4 o;
 #pragma unroll
             for (int e = 0; e < 4; e++)
@@ -158,8 +173,18 @@ __device__ __forceinline__ void ti_finish(const I8Args &a, const uint8_t *w, int
                 for (int e = 0; e < 4; e++)
                     o[e] = silu(o[e]) * ((float)u[e] * xs * tu[e]);
             }
-            if (b0 + row < rows)
-                i8_put4_part<OUTT>(to, o, left);
+            return o;
+        };
+        if (b0 + GR <= rows && n - c * 4 + TO * 16 <= a.ncols) {  // uniform: all inside, four rows' reads at once
+#pragma unroll 4
+            for (int k = 0; k < GR / RPI; k++, to += next)
+                i8_put4<OUTT>(to, out(k * RPI + r));
+        } else {
+            for (int k = 0; k < GR / RPI; k++, to += next) {
+                const f32x4 o = out(k * RPI + r);
+                if (b0 + k * RPI + r < rows)
+                    i8_put4_part<OUTT>(to, o, left);
+            }
         }
     }
 }
@@ -430,8 +455,9 @@ __device__ __forceinline__ void ti_whole(const I8Args &a, int mt, int nt, const 
     if (rows <= 0 || nt * (S::BN / (DUAL ? 2 : 1)) >= a.ncols)
         return;  // uniform: a piece of a tile that lies outside
     i32x4 acc[S::TM][S::TN];
+    const TiScales<S, DUAL> sc(a, a.w, row0, rows, nt);
     ti_tile_sums<S, DUAL>(a, a.w, row0, rows, nt, 0, a.S, lds, acc);
-    ti_finish<S, DUAL, OUTT>(a, a.w, row0, rows, nt,
+    ti_finish<S, DUAL, OUTT>(a, sc, row0, rows, nt,
                              ti_own<S>(lds, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), acc);
 }
 
@@ -466,6 +492,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int m
     const int64_t row0 = (int64_t)mt * S::BM;
     const int rows = min(S::BM, (int)(a.B - row0));
     i32x4 acc[S::TM][S::TN];
+    const TiScales<S, DUAL> sc(a, a.w, row0, rows, nt);
     TI_SUMS(S, DUAL, a, a.w, row0, rows, nt, k0, k1)
     const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
     if (split > 1) {
@@ -477,7 +504,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_tiled_kernel(I8Args a, int m
                 p[(i * S::TN + j) * 64 + lane] = acc[i][j];
         return;
     }
-    ti_finish<S, DUAL, OUTT>(a, a.w, row0, rows, nt, own, acc);
+    ti_finish<S, DUAL, OUTT>(a, sc, row0, rows, nt, own, acc);
 }
 
 // The split's partial tiles, a wave a row group of a wave's part of a tile.
@@ -575,8 +602,9 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
     const int rows = min(S::BM, __builtin_amdgcn_readfirstlane(found[2]) - row0);
     const uint8_t *w = uniform_ptr(grp.wtab[e]);
     i32x4 acc[S::TM][S::TN];
+    const TiScales<S, DUAL> sc(a, w, row0, rows, nt);
     TI_SUMS(S, DUAL, a, w, row0, rows, nt, 0, a.S)
-    ti_finish<S, DUAL, OUTT>(a, w, row0, rows, nt, own, acc);
+    ti_finish<S, DUAL, OUTT>(a, sc, row0, rows, nt, own, acc);
 }
 
 // ------------------------------------------------------------------ host
