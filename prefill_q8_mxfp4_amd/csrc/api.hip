@@ -1412,7 +1412,7 @@ int qgemm_route(int64_t E, int64_t T, int64_t topk, const int32_t *ids, int32_t 
         return fail(QGEMM_EINVAL, "qgemm_route: null pointer");
     if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)pos) & 3u)
         return fail(QGEMM_EINVAL, "qgemm_route: misaligned pointer");
-    RouteArgs a = {ids, offsets, pos, (int)(T * topk), (int)E};
+    RouteArgs a = {ids, offsets, pos, (int)(T * topk), (int)E, false};
     const hipError_t e = launch_route(a, (hipStream_t)stream);
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_route: kernel launch");
 }

@@ -127,8 +127,9 @@ struct RouteArgs {
     const int *ids;
     int *off, *pos;
     int n, E;
+    bool vec;  // ids are 16-byte aligned
 };
-hipError_t launch_route(const RouteArgs &a, hipStream_t st);
+hipError_t launch_route(RouteArgs a, hipStream_t st);
 
 struct MoveArgs {
     const void *src, *src2;  // dispatch: x; combine: ys; combine_grad: dy, ys

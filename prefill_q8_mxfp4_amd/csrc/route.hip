@@ -31,14 +31,31 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs a, int run,
     for (int e = tid; e < 2 * a.E; e += RT_THREADS)
         lds[e] = 0;
     __syncthreads();
-    for (int f = tid; f < a.n; f += RT_THREADS) {
-        const int e = a.ids[f];
+    auto count = [&](int f, int e) {
         if (e >= 0 && e < a.E) {
             atomicAdd(&tot[e], 1);
             if (f < lo)
                 atomicAdd(&mine[e], 1);
         }
+    };
+    // four ids a load, four loads in flight
+    const int quads = a.vec ? a.n / 4 : 0;
+    for (int q0 = tid; q0 < quads; q0 += 4 * RT_THREADS) {
+        typedef int i32x4v __attribute__((ext_vector_type(4)));
+        i32x4v v[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int q = q0 + k * RT_THREADS;
+            v[k] = q < quads ? ((const i32x4v *)a.ids)[q] : i32x4v{-1, -1, -1, -1};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                count((q0 + k * RT_THREADS) * 4 + i, v[k][i]);
     }
+    for (int f = quads * 4 + tid; f < a.n; f += RT_THREADS)
+        count(f, a.ids[f]);
     __syncthreads();
     // exclusive scan of tot over the experts, RT_THREADS of them at a time
     int carry = 0;
@@ -83,7 +100,8 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs a, int run,
         const int rank = __popcll(same & ((1ull << lane) - 1));
         const bool first = kept && rank == 0;
         int base = 0;
-        for (int w = 0; w < RT_WAVES; w++) {  // waves in order
+        const int waves = min(RT_WAVES, (hi - f0 + 63) / 64);
+        for (int w = 0; w < waves; w++) {  // waves in order
             if (w == wid && first)
                 base = atomicAdd(&mine[id], __popcll(same));
             __syncthreads();
@@ -94,14 +112,17 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs a, int run,
     }
 }
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t st)
+hipError_t launch_route(RouteArgs a, hipStream_t st)
 {
     int bits = 0;
     while (bits < 31 && (1 << bits) < a.E)
         bits++;
-    const int runs = a.n < 64 * RT_THREADS ? (a.n + RT_THREADS - 1) / RT_THREADS : 64;
-    const int wgs = runs < 1 ? 1 : runs;
-    const int run = (a.n + wgs - 1) / wgs;
+    // runs of 256 choices, up to 256 of them: the count of all choices, which every
+    // workgroup makes, is most of the time, the places of a run the rest
+    int run = (a.n + 255) / 256;
+    run = run < 256 ? 256 : (run + 63) / 64 * 64;
+    const int wgs = a.n > 0 ? (a.n + run - 1) / run : 1;
+    a.vec = ((uintptr_t)a.ids & 15u) == 0;
     const int lds = 2 * a.E * 4;
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute((const void *)route_kernel,
@@ -116,7 +137,8 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t st)
 // ================================================================ moves
 // A row is cut into 16-byte vectors; rows whose size is no multiple of 16
 // start off alignment, which gfx950's global loads and stores take, and end in
-// single elements.
+// single elements.  Moving bytes is the bound: a wave owns 64 vectors of a token
+// and has the loads of several of its rows in flight.
 template <int DT>
 struct Elem {
     typedef float T;
@@ -128,132 +150,188 @@ struct Elem<OUT_BF16> {
     static constexpr int V = 8;
 };
 
+// A vector as it is, its first `left` elements (the others zero).
 template <int DT>
-__device__ __forceinline__ void load_vec(const typename Elem<DT>::T *p, int left, float *v)
+__device__ __forceinline__ u32x4 load_raw(const typename Elem<DT>::T *p, int left)
 {
-    constexpr int V = Elem<DT>::V;
-    typename Elem<DT>::T e[V];
-    if (left >= V) {
-        __builtin_memcpy(e, p, 16);
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = (float)e[i];
+    u32x4 r = u32x4{0u, 0u, 0u, 0u};
+    if (left >= Elem<DT>::V) {
+        __builtin_memcpy(&r, p, 16);
     } else {
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            v[i] = i < left ? (float)p[i] : 0.f;
+        for (int i = 0; i < Elem<DT>::V - 1; i++) {
+            if (i < left) {
+                if constexpr (DT == OUT_F32)
+                    r[i] = __float_as_uint(p[i]);
+                else
+                    r[i / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (i & 1));
+            }
+        }
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float elem_of(u32x4 r, int i)
+{
+    if constexpr (DT == OUT_F32)
+        return __uint_as_float(r[i]);
+    else
+        return __uint_as_float(i & 1 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_raw(typename Elem<DT>::T *p, int left, u32x4 r)
+{
+    if (left >= Elem<DT>::V) {
+        __builtin_memcpy(p, &r, 16);
+    } else {
+        for (int i = 0; i < Elem<DT>::V - 1; i++) {
+            if (i < left) {
+                if constexpr (DT == OUT_F32)
+                    p[i] = __uint_as_float(r[i]);
+                else
+                    ((uint16_t *)p)[i] = (uint16_t)(r[i / 2] >> (16 * (i & 1)));
+            }
+        }
     }
 }
 
 template <int DT>
-__device__ __forceinline__ void store_vec(typename Elem<DT>::T *p, int left, const float *v)
+__device__ __forceinline__ u32x4 pack_vec(const float *v)
 {
-    constexpr int V = Elem<DT>::V;
-    typename Elem<DT>::T e[V];
+    typename Elem<DT>::T e[Elem<DT>::V];
 #pragma unroll
-    for (int i = 0; i < V; i++)
+    for (int i = 0; i < Elem<DT>::V; i++)
         e[i] = (typename Elem<DT>::T)v[i];
-    if (left >= V) {
-        __builtin_memcpy(p, e, 16);
-    } else {
-        for (int i = 0; i < V; i++)
-            if (i < left)
-                p[i] = e[i];
-    }
+    u32x4 r;
+    __builtin_memcpy(&r, e, 16);
+    return r;
 }
 
 // The row a choice names: -1 for a dropped one; one past the rows is reported
 // and treated as dropped.
-__device__ __forceinline__ int64_t row_of(const MoveArgs &a, int64_t f)
+__device__ __forceinline__ int row_of(const MoveArgs &a, int64_t f)
 {
     const int p = a.pos[f];
-    if (p < 0)
-        return -1;
     if (p >= a.R) {
         __hip_atomic_fetch_or(a.status, DEV_BAD_ROUTE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         return -1;
     }
-    return p;
+    return p < 0 ? -1 : p;
 }
 
-// dispatch: xs[pos[t][j]] = x[t].  A wave owns 64 vectors of one token's row:
-// one load, topk stores.
+// dispatch: xs[pos[t][j]] = x[t].  One load, topk stores; lane j reads choice j.
 template <int DT>
-__global__ __launch_bounds__(64) void dispatch_kernel(MoveArgs a)
+__global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a, int chunks)
 {
     typedef typename Elem<DT>::T E;
     constexpr int V = Elem<DT>::V;
-    const int64_t t = blockIdx.x;
-    const int64_t h = ((int64_t)blockIdx.y * 64 + threadIdx.x) * V;
+    const int lane = threadIdx.x & 63;
+    const int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = u / chunks;
+    if (t >= a.T)
+        return;
+    const int64_t h = (u % chunks * 64 + lane) * V;
     const int left = (int)min((int64_t)V, a.H - h);
-    float v[V];
+    const int mine = lane < a.topk ? row_of(a, t * a.topk + lane) : -1;
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (left > 0)
-        load_vec<DT>((const E *)a.src + t * a.H + h, left, v);
+        v = load_raw<DT>((const E *)a.src + t * a.H + h, left);
     for (int j = 0; j < a.topk; j++) {
-        const int64_t p = row_of(a, t * a.topk + j);
+        const int p = __builtin_amdgcn_readlane(mine, j);
         if (p >= 0 && left > 0)
-            store_vec<DT>((E *)a.dst + p * a.H + h, left, v);
+            store_raw<DT>((E *)a.dst + (int64_t)p * a.H + h, left, v);
     }
 }
 
 // combine: y[t] = sum_j w[t][j] ys[pos[t][j]], j in order, fp32, one rounding.
+// Eight choices' loads in flight; lane j reads choice j and its weight.
 template <int DT>
-__global__ __launch_bounds__(64) void combine_kernel(MoveArgs a)
+__global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int chunks)
 {
     typedef typename Elem<DT>::T E;
-    constexpr int V = Elem<DT>::V;
-    const int64_t t = blockIdx.x;
-    const int64_t h = ((int64_t)blockIdx.y * 64 + threadIdx.x) * V;
+    constexpr int V = Elem<DT>::V, G = 8;
+    const int lane = threadIdx.x & 63;
+    const int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = u / chunks;
+    if (t >= a.T)
+        return;
+    const int64_t h = (u % chunks * 64 + lane) * V;
     const int left = (int)min((int64_t)V, a.H - h);
+    const int64_t f = t * a.topk + lane;
+    const int mine = lane < a.topk ? row_of(a, f) : -1;
+    const float wl = a.weights && lane < a.topk ? a.weights[f] : 1.f;
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; i++)
         sum[i] = 0.f;
-    for (int j = 0; j < a.topk; j++) {
-        const int64_t p = row_of(a, t * a.topk + j);
-        if (p >= 0 && left > 0) {
-            const float w = a.weights ? a.weights[t * a.topk + j] : 1.f;
-            float v[V];
-            load_vec<DT>((const E *)a.src + p * a.H + h, left, v);
+    for (int j0 = 0; j0 < a.topk; j0 += G) {
+        u32x4 v[G];
+        int p[G];
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                sum[i] = fmaf(w, v[i], sum[i]);
+        for (int g = 0; g < G; g++) {
+            p[g] = j0 + g < a.topk ? __builtin_amdgcn_readlane(mine, j0 + g) : -1;
+            if (p[g] >= 0 && left > 0)
+                v[g] = load_raw<DT>((const E *)a.src + (int64_t)p[g] * a.H + h, left);
         }
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            if (p[g] >= 0) {
+                const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), (j0 + g) & 63));
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    sum[i] = fmaf(w, elem_of<DT>(v[g], i), sum[i]);
+            }
     }
     if (left > 0)
-        store_vec<DT>((E *)a.dst + t * a.H + h, left, sum);
+        store_raw<DT>((E *)a.dst + t * a.H + h, left, pack_vec<DT>(sum));
 }
 
 // combine_grad, one wave a choice: dys[p] = w dy[t], dw = sum_h dy[t][h] ys[p][h].
+// Two vectors of both rows in flight; neighbouring waves share dy in L1.
 template <int DT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(MoveArgs a)
 {
     typedef typename Elem<DT>::T E;
-    constexpr int V = Elem<DT>::V;
-    const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    constexpr int V = Elem<DT>::V, G = 2;
+    const int64_t f = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (f >= a.T * a.topk)
         return;
     const int64_t t = f / a.topk;
-    const int64_t p = row_of(a, f);
+    const int64_t p = __builtin_amdgcn_readfirstlane(row_of(a, f));
     float dot = 0.f;
     if (p >= 0) {
         const float w = a.weights[f];
         const E *dy = (const E *)a.src + t * a.H;
         const E *ys = (const E *)a.src2 + p * a.H;
         E *dys = (E *)a.dst + p * a.H;
-        for (int64_t h = lane * V; h < a.H; h += 64 * V) {
-            const int left = (int)min((int64_t)V, a.H - h);
-            float g[V], y[V];
-            load_vec<DT>(dy + h, left, g);
-            load_vec<DT>(ys + h, left, y);
+        for (int64_t h0 = lane * V; h0 < a.H; h0 += 64 * V * G) {
+            u32x4 g[G], y[G];
+            int left[G];
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                if (i < left)
-                    dot = fmaf(g[i], y[i], dot);
-                g[i] *= w;
+            for (int k = 0; k < G; k++) {
+                const int64_t h = h0 + 64 * V * k;
+                left[k] = (int)min((int64_t)V, a.H - h);
+                if (left[k] > 0) {
+                    g[k] = load_raw<DT>(dy + h, left[k]);
+                    y[k] = load_raw<DT>(ys + h, left[k]);
+                }
             }
-            store_vec<DT>(dys + h, left, g);
+#pragma unroll
+            for (int k = 0; k < G; k++) {
+                if (left[k] > 0) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; i++) {
+                        const float d = elem_of<DT>(g[k], i);
+                        if (i < left[k])
+                            dot = fmaf(d, elem_of<DT>(y[k], i), dot);
+                        o[i] = w * d;
+                    }
+                    store_raw<DT>(dys + h0 + 64 * V * k, left[k], pack_vec<DT>(o));
+                }
+            }
         }
     }
     for (int d = 32; d; d >>= 1)
@@ -262,28 +340,28 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(MoveArgs a)
         a.dw[f] = dot;
 }
 
-template <int DT>
-static dim3 vec_grid(const MoveArgs &a)
+template <int DT, typename K>
+static void go_by_vectors(K kernel, const MoveArgs &a, hipStream_t st)
 {
-    const int64_t per = 64 * Elem<DT>::V;
-    return dim3((unsigned)a.T, (unsigned)((a.H + per - 1) / per));
+    const int64_t per = 64 * Elem<DT>::V, chunks = (a.H + per - 1) / per;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T * chunks + 3) / 4)), dim3(256), 0, st, a, (int)chunks);
 }
 
 hipError_t launch_dispatch(int dt, const MoveArgs &a, hipStream_t st)
 {
     if (dt == OUT_F32)
-        hipLaunchKernelGGL(dispatch_kernel<OUT_F32>, vec_grid<OUT_F32>(a), dim3(64), 0, st, a);
+        go_by_vectors<OUT_F32>(dispatch_kernel<OUT_F32>, a, st);
     else
-        hipLaunchKernelGGL(dispatch_kernel<OUT_BF16>, vec_grid<OUT_BF16>(a), dim3(64), 0, st, a);
+        go_by_vectors<OUT_BF16>(dispatch_kernel<OUT_BF16>, a, st);
     return hipGetLastError();
 }
 
 hipError_t launch_combine(int dt, const MoveArgs &a, hipStream_t st)
 {
     if (dt == OUT_F32)
-        hipLaunchKernelGGL(combine_kernel<OUT_F32>, vec_grid<OUT_F32>(a), dim3(64), 0, st, a);
+        go_by_vectors<OUT_F32>(combine_kernel<OUT_F32>, a, st);
     else
-        hipLaunchKernelGGL(combine_kernel<OUT_BF16>, vec_grid<OUT_BF16>(a), dim3(64), 0, st, a);
+        go_by_vectors<OUT_BF16>(combine_kernel<OUT_BF16>, a, st);
     return hipGetLastError();
 }
 
