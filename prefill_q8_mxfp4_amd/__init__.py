@@ -313,7 +313,9 @@ class Plan:
         if w.numel() < self.weight_bytes:
             raise ValueError("packed weight buffer too small")
         if self.fmt == "int8":
-            return self._run_int8(x, w, y, stream, B, workspace)
+            from . import _rows
+
+            return _rows.run(self, x, w, y, stream, B, workspace)
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         init_device(x.device)
@@ -374,72 +376,17 @@ class Plan:
         """qgemm_run_codes: y = the int8 product of rows that are codes
         already (quantize_rows): codes int8 [B][K], rows 16-byte aligned at
         any pitch; scales float32 [B].  workspace as in run()."""
-        import torch
+        from . import _rows
 
-        B, ldc = _codes_pitch(codes, scales, self.K)
-        want_y = torch.float32 if self.out == "f32" else torch.bfloat16
-        if y.dtype != want_y or w.dtype != torch.uint8:
-            raise TypeError("dtype mismatch: w %s, y %s" % (w.dtype, y.dtype))
-        if y.numel() < B * self.out_cols:
-            raise ValueError("y too small for B")
-        if w.numel() < self.weight_bytes:
-            raise ValueError("packed weight buffer too small")
-        dev = _gpu(codes)
-        wsp, wsn = self._workspace_of(workspace, B, dev, stream, codes=True)
-        _call(lib().qgemm_run_codes, dev, stream, self._h, B, _addr(w, "w", dev), codes.data_ptr(), ldc,
-              _addr(scales, "scales", dev), _addr(y, "y", dev), wsp, wsn)
-        return y
-
-    def _run_int8(self, x, w, y, stream, B, workspace):
-        """run() of int8 weights: the rows are quantised into the workspace."""
-        dev = _gpu(x)
-        wsp, wsn = self._workspace_of(workspace, B, dev, stream)
-        _call(lib().qgemm_run_ws, dev, stream, self._h, B, _addr(w, "w", dev), _addr(x, "x", dev), _addr(y, "y", dev),
-              wsp, wsn)
-        return y
-
-    def _workspace_of(self, workspace, B, dev, stream, codes=False):
-        """(address, bytes) of an int8 call's workspace: the caller's, none, or
-        ("auto") the plan's.  The plan's is asked for again only when the width,
-        the device or the stream is not the last call's."""
-        import torch
-
-        if workspace is None:
-            return 0, 0
-        if not isinstance(workspace, str):
-            return _addr(workspace, "workspace", dev), workspace.numel()
-        if B == 0:
-            return 0, 0
-        if codes and self.tier(B) == "skinny":
-            return 0, 0                     # nothing to split or to quantise
-        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-        key = (B, dev, raw)
-        last = self.__dict__.get("_ws_last")
-        if last is None or last[0] != key or torch.cuda.is_current_stream_capturing():
-            st = torch.cuda.current_stream(dev) if stream is None else stream
-            ws = self._workspace(B, torch.device("cuda", dev), st)
-            last = self._ws_last = (key, ws.data_ptr(), ws.numel())
-        return last[1], last[2]
+        return _rows.run_codes(self, codes, scales, w, y, stream, workspace)
 
     def run_grouped_codes(self, codes, scales, w_table, offsets, y, stream=None):
         """qgemm_run_grouped_codes: routed experts on rows of codes sorted by
         expert (route, dispatch_codes); w_table and offsets as in
         run_grouped.  Rows from offsets[E] on are left as they were."""
-        import torch
+        from . import _rows
 
-        T, ldc = _codes_pitch(codes, scales, self.K)
-        E = w_table.numel()
-        want_y = torch.float32 if self.out == "f32" else torch.bfloat16
-        if y.dtype != want_y:
-            raise TypeError("dtype mismatch: y %s" % y.dtype)
-        if w_table.dtype != torch.int64 or offsets.dtype != torch.int32 or offsets.numel() != E + 1:
-            raise TypeError("w_table must be int64 [E], offsets int32 [E + 1]")
-        if y.numel() < T * self.out_cols:
-            raise ValueError("y too small")
-        dev = _gpu(codes)
-        _call(lib().qgemm_run_grouped_codes, dev, stream, self._h, E, T, _addr(w_table, "w_table", dev),
-              _addr(offsets, "offsets", dev), codes.data_ptr(), ldc, _addr(scales, "scales", dev), _addr(y, "y", dev))
-        return y
+        return _rows.run_grouped_codes(self, codes, scales, w_table, offsets, y, stream)
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -453,256 +400,19 @@ class Plan:
             pass
 
 
-class _on_device:
-    """The tensors' device as the current one inside the block (kernels, the
-    status word and streams belong to it); only entered when it is another."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        import torch
-
-        self.before = torch.cuda.current_device()
-        torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        import torch
-
-        torch.cuda.set_device(self.before)
+# The 8-bit rows and products and the row movements live in _rows.py, which
+# imports torch; the names are the package's.
+_ROWS = ("code_stride", "pack_int8", "quantize_rows", "route", "dispatch", "dispatch_codes", "dispatch_grad", "combine",
+         "combine_grad")
 
 
-def _gpu(t):
-    """Index of a tensor's GPU."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA (HIP) device")
-    return dev
+def __getattr__(name):
+    if name in _ROWS:
+        from . import _rows
 
-
-def _addr(t, name, dev):
-    """Address of a contiguous tensor on GPU dev."""
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the CUDA (HIP) device of the others" % name)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
-
-
-def _call(f, dev, stream, *args):
-    """One call of an entry point whose last argument is the stream, on GPU
-    dev.  A call costs a few microseconds of host time, which bounds the small
-    ones: the raw stream is asked for (0.1 us) rather than a Stream object (2 us)."""
-    import torch
-
-    if torch.cuda.current_device() != dev:
-        with _on_device(dev):
-            return _call(f, dev, stream, *args)
-    status = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-    if status != OK:
-        _check(status)
-
-
-def code_stride(K: int) -> int:
-    """The pitch at which quantize_rows allocates rows of K codes."""
-    return (K + 15) // 16 * 16
-
-
-def _codes_pitch(codes, scales, K):
-    """(rows, pitch) of a tensor of codes, checked with its scales."""
-    import torch
-
-    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
-        raise TypeError("codes must be int8 and scales float32, not %s and %s" % (codes.dtype, scales.dtype))
-    if codes.dim() != 2 or codes.shape[1] != K:
-        raise ValueError("codes must be [rows][%d], not %s" % (K, tuple(codes.shape)))
-    B = codes.shape[0]
-    # one row, or none, carries no pitch of its own
-    ldc = codes.stride(0) if B > 1 else max(codes.stride(0), code_stride(K))
-    if (K > 1 and codes.stride(1) != 1) or ldc % 16 or ldc < K:
-        raise ValueError("codes must be rows of stride 1 at a pitch that is a multiple of 16 and at least K")
-    if B and codes.untyped_storage().nbytes() - codes.storage_offset() < B * ldc:
-        raise ValueError("the last row of codes must have room for its whole pitch (%d bytes)" % ldc)
-    if scales.numel() < B:
-        raise ValueError("scales too small")
-    return B, ldc
-
-
-def _codes_addr(codes, dev):
-    if codes.get_device() != dev:
-        raise ValueError("codes must be on the CUDA (HIP) device of the others")
-    return codes.data_ptr()
-
-
-def _rows_dtype(t, name):
-    import torch
-
-    if t.dtype == torch.float32:
-        return 0
-    if t.dtype == torch.bfloat16:
-        return 1
-    raise TypeError("%s must be float32 or bfloat16, not %s" % (name, t.dtype))
-
-
-def pack_int8(codes, scales, out=None, stream=None):
-    """qgemm_pack_device: int8 codes [N][K] and float32 scales [N] on the GPU
-    to the packed buffer (uint8, allocated unless given)."""
-    import torch
-
-    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
-        raise TypeError("codes must be int8 and scales float32, not %s and %s" % (codes.dtype, scales.dtype))
-    if codes.dim() != 2 or scales.shape != codes.shape[:1]:
-        raise ValueError("codes must be [N][K], scales [N]")
-    N, K = codes.shape
-    nbytes = weight_bytes("int8", N, K)
-    if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
-    if out.dtype != torch.uint8 or out.numel() < nbytes:
-        raise ValueError("out must be uint8, at least %d bytes" % nbytes)
-    dev = _gpu(codes)
-    _call(lib().qgemm_pack_device, dev, stream, FORMATS["int8"], N, K, _addr(codes, "codes", dev),
-          _addr(scales, "scales", dev), _addr(out, "out", dev), out.numel())
-    return out
-
-
-def _new_codes(R, K, device):
-    import torch
-
-    return torch.empty((R, code_stride(K)), dtype=torch.int8, device=device)[:, :K]
-
-
-def quantize_rows(x, codes=None, scales=None, stream=None):
-    """qgemm_quantize_rows: float32 or bfloat16 rows x [B][K] to int8 codes
-    [B][K] (at a pitch of code_stride(K)) and float32 scales [B]; outputs are
-    allocated unless given."""
-    import torch
-
-    dt = _rows_dtype(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [B][K]")
-    B, K = x.shape
-    if codes is None:
-        codes = _new_codes(B, K, x.device)
-    if scales is None:
-        scales = torch.empty(B, dtype=torch.float32, device=x.device)
-    rows, ldc = _codes_pitch(codes, scales, K)
-    if rows != B:
-        raise ValueError("codes must have x's rows")
-    dev = _gpu(x)
-    _call(lib().qgemm_quantize_rows, dev, stream, dt, B, K, _addr(x, "x", dev), _codes_addr(codes, dev), ldc,
-          _addr(scales, "scales", dev))
-    return codes, scales
-
-
-def route(ids, E: int, offsets=None, pos=None, stream=None):
-    """qgemm_route: the router's choices ids (int32 [T][topk]; ids outside
-    0..E-1 are dropped) to the offsets (int32 [E + 1]) that run_grouped and
-    run_grouped_codes take and the sorted row of each choice, pos (int32
-    [T][topk], -1 for a dropped one); outputs are allocated unless given."""
-    import torch
-
-    if ids.dtype != torch.int32 or ids.dim() != 2:
-        raise TypeError("ids must be int32 [T][topk]")
-    if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
-    if pos is None:
-        pos = torch.empty_like(ids)
-    if offsets.dtype != torch.int32 or pos.dtype != torch.int32:
-        raise TypeError("offsets and pos must be int32")
-    if offsets.numel() != E + 1 or pos.shape != ids.shape:
-        raise ValueError("offsets must be [E + 1], pos as ids")
-    dev = _gpu(ids)
-    _call(lib().qgemm_route, dev, stream, E, ids.shape[0], ids.shape[1], _addr(ids, "ids", dev),
-          _addr(offsets, "offsets", dev), _addr(pos, "pos", dev))
-    return offsets, pos
-
-
-def _check_pos(pos, T):
-    import torch
-
-    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[0] != T:
-        raise TypeError("pos must be int32 [T][topk]")
-
-
-def _check_weights(weights, pos, name="weights"):
-    import torch
-
-    if weights.dtype != torch.float32 or weights.shape != pos.shape:
-        raise TypeError("%s must be float32 [T][topk]" % name)
-
-
-def _check_rows(rows, like, name):
-    if rows.dtype != like.dtype:
-        raise TypeError("dtype mismatch: %s %s" % (name, rows.dtype))
-    if rows.dim() != 2 or rows.shape[1] != like.shape[1]:
-        raise ValueError("%s must be rows of %d" % (name, like.shape[1]))
-
-
-def dispatch(x, pos, xs, stream=None):
-    """qgemm_dispatch: xs[pos[t][j]] = x[t], x [T][H] and xs [R][H] float32
-    or bfloat16.  Rows of xs that no choice names are left as they were."""
-    dt = _rows_dtype(x, "x")
-    _check_rows(xs, x, "xs")
-    _check_pos(pos, x.shape[0])
-    dev = _gpu(x)
-    _call(lib().qgemm_dispatch, dev, stream, dt, x.shape[0], pos.shape[1], x.shape[1], xs.shape[0],
-          _addr(x, "x", dev), _addr(pos, "pos", dev), _addr(xs, "xs", dev))
-    return xs
-
-
-def dispatch_codes(x, pos, codes, scales, stream=None):
-    """qgemm_dispatch_codes: quantize_rows and dispatch in one pass: x [T][K]
-    to the sorted rows of codes [R][K] and scales [R]."""
-    dt = _rows_dtype(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [T][K]")
-    _check_pos(pos, x.shape[0])
-    R, ldc = _codes_pitch(codes, scales, x.shape[1])
-    dev = _gpu(x)
-    _call(lib().qgemm_dispatch_codes, dev, stream, dt, x.shape[0], pos.shape[1], x.shape[1], R, _addr(x, "x", dev),
-          _addr(pos, "pos", dev), _codes_addr(codes, dev), ldc, _addr(scales, "scales", dev))
-    return codes, scales
-
-
-def combine(ys, pos, weights, y, stream=None):
-    """qgemm_combine: y[t] = sum_j weights[t][j] * ys[pos[t][j]], ys [R][H]
-    and y [T][H] float32 or bfloat16, weights float32 [T][topk] or None (ones)."""
-    dt = _rows_dtype(ys, "ys")
-    _check_rows(y, ys, "y")
-    _check_pos(pos, y.shape[0])
-    if weights is not None:
-        _check_weights(weights, pos)
-    dev = _gpu(ys)
-    wp = None if weights is None else _addr(weights, "weights", dev)
-    _call(lib().qgemm_combine, dev, stream, dt, y.shape[0], pos.shape[1], y.shape[1], ys.shape[0],
-          _addr(ys, "ys", dev), _addr(pos, "pos", dev), wp, _addr(y, "y", dev))
-    return y
-
-
-def dispatch_grad(dxs, pos, dx, stream=None):
-    """The gradient of dispatch: dx[t] = sum_j dxs[pos[t][j]]."""
-    return combine(dxs, pos, None, dx, stream)
-
-
-def combine_grad(dy, ys, pos, weights, dys, dw, stream=None):
-    """qgemm_combine_grad: dys[pos[t][j]] = weights[t][j] * dy[t] and
-    dw[t][j] = dy[t] . ys[pos[t][j]] (float32, 0 for a dropped choice); rows
-    of dys that no choice names are left as they were."""
-    dt = _rows_dtype(dy, "dy")
-    _check_rows(ys, dy, "ys")
-    _check_rows(dys, dy, "dys")
-    _check_pos(pos, dy.shape[0])
-    _check_weights(weights, pos)
-    _check_weights(dw, pos, "dw")
-    if dys.shape[0] != ys.shape[0]:
-        raise ValueError("dys must have ys's rows")
-    dev = _gpu(dy)
-    _call(lib().qgemm_combine_grad, dev, stream, dt, dy.shape[0], pos.shape[1], dy.shape[1], ys.shape[0],
-          _addr(dy, "dy", dev), _addr(ys, "ys", dev), _addr(pos, "pos", dev), _addr(weights, "weights", dev),
-          _addr(dys, "dys", dev), _addr(dw, "dw", dev))
-    return dys, dw
+        globals().update({n: getattr(_rows, n) for n in _ROWS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def dequantize(fmt: str, w, N: int, K: int, stream=None):

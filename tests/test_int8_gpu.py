@@ -539,7 +539,7 @@ def layer(x, ids, weights, E, gu_plan, gu_table, dn_plan, dn_table, st=None):
     T, k = ids.shape
     R, H, nh = T * k, x.shape[1], gu_plan.out_cols
     off, pos = q.route(ids, E, stream=st)
-    codes, scales = q._new_codes(R, H, x.device), torch.empty(R, device=x.device)
+    codes, scales = torch.empty((R, q.code_stride(H)), dtype=torch.int8, device=x.device)[:, :H], torch.empty(R, device=x.device)
     q.dispatch_codes(x, pos, codes, scales, stream=st)
     h = torch.zeros(R, nh, dtype=torch.bfloat16, device=x.device)
     gu_plan.run_grouped_codes(codes, scales, gu_table, off, h, stream=st)
