@@ -24,7 +24,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 UNITS = ("api.hip", "skinny.hip", "stream.hip", "tiled.hip", "tiled_w4.hip", "tiled_fp32.hip", "dequant.hip",
          "readbw.hip", "gemv.hip", "mfma_rate.hip", "moe.hip", "verify.hip",
          "verify_bf16.hip", "int8_rows.hip", "int8_small.hip", "int8_tiled.hip", "route.hip")
-HEADERS = ("common.h", "layout.h", "tiled.h", "verify.h", "verify_launch.h", "int8.h")
+HEADERS = ("common.h", "layout.h", "tiled.h", "verify.h", "verify_launch.h", "int8.h", "int8_quant.h")
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -969,6 +969,10 @@ static int run_with(const qgemm_plan *plan, int64_t B, const void *w, const void
             return fail(QGEMM_ENOTSUP, "qgemm_run: QGEMM_INT8 quantises the rows into a workspace of "
                                        "qgemm_workspace_bytes (qgemm_run_ws or qgemm_run_noalloc), or takes codes "
                                        "(qgemm_run_codes)");
+        if (i8_tier(plan, B) == QGEMM_TIER_SKINNY && i8_small_fuses(B, p.K, p.L.S)) {
+            const hipError_t e = launch_i8_small_fused(i8_args(p, B, w, nullptr, 0, nullptr, y), x, p.act, p.out, st);
+            return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run: kernel launch");
+        }
         // partial tiles first: at the size they may have, or none at all
         const int64_t pb = i8_part_bytes(plan, B) <= room ? i8_part_bytes(plan, B) : 0;
         RowsArgs r = {};

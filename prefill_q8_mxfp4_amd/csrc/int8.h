@@ -101,6 +101,9 @@ hipError_t launch_i8_pack(const Layout &L, const int8_t *codes, const float *sca
 // ---- int8_small.hip: few rows, weights streamed into the operands
 hipError_t launch_i8_small(const I8Args &a, int outt, hipStream_t st);
 bool i8_small_wins(int64_t B, int64_t N);  // the automatic choice
+// rows x of type act, quantised on the way (codes and xs are not read)
+bool i8_small_fuses(int64_t B, int64_t K, int64_t S);
+hipError_t launch_i8_small_fused(const I8Args &a, const void *x, int act, int outt, hipStream_t st);
 
 // ---- int8_tiled.hip: many rows, tiles through LDS
 enum I8Shape {  // batch rows x channels of a tile

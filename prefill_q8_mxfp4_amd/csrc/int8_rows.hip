@@ -6,97 +6,56 @@
 // with both quotients correctly rounded; s = 0 gives q = 0, and a row that
 // holds a NaN or an infinity gets s = NaN and q = 0, so that its products are
 // NaN.  Columns K .. ldc-1 of the codes are written as zero.
-#include "int8.h"
+#include "int8_quant.h"
 
 namespace qg {
 
-constexpr int RQ_V = 8;  // elements of a thread's vector
-
-template <int ACT>
-__device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, float *v)
-{
-    if (left >= RQ_V) {
-        if constexpr (ACT == ACT_F32) {
-            __builtin_memcpy(v, (const float *)x + at, 32);
-        } else {
-            uint16_t h[RQ_V];
-            __builtin_memcpy(h, (const uint16_t *)x + at, 16);
-#pragma unroll
-            for (int i = 0; i < RQ_V; i++)
-                v[i] = __uint_as_float((uint32_t)h[i] << 16);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < RQ_V; i++) {
-            v[i] = 0.f;
-            if (i < left)
-                v[i] = ACT == ACT_F32 ? ((const float *)x)[at + i]
-                                      : __uint_as_float((uint32_t)((const uint16_t *)x)[at + i] << 16);
-        }
-    }
-}
-
-// Eight codes.  x * (1 / s) is within 2^-15 of the quotient that the definition
-// rounds (|x / s| <= 127.5, three roundings of 2^-23 of it at most), so only a
-// value that near to a border between codes, or one that is no number because
-// 1 / s overflowed, takes the division (ten instructions each: 19 against 15 us
-// for 2048 rows of 5120).
-__device__ __forceinline__ u32x2 pack_codes8(const float *v, float s, float inv)
-{
-    float n[RQ_V];
-    bool near = false;
-#pragma unroll
-    for (int i = 0; i < RQ_V; i++) {
-        const float r = v[i] * inv;
-        n[i] = __builtin_rintf(r);
-        near |= !(__builtin_fabsf(r - n[i]) < 0.4999f);
-    }
-    if (near) {
-#pragma unroll
-        for (int i = 0; i < RQ_V; i++)
-            n[i] = __builtin_rintf(v[i] / s);
-    }
-    u32x2 o = u32x2{0u, 0u};
-#pragma unroll
-    for (int i = 0; i < RQ_V; i++) {
-        const int c = (int)fminf(fmaxf(n[i], -127.f), 127.f);
-        o[i / 4] |= ((uint32_t)c & 0xFFu) << (8 * (i % 4));
-    }
-    return o;
-}
-
 // TPR threads a row (64: four rows a workgroup and no barrier), the row held in
 // NV vectors of registers a thread as far as it fits, the rest read twice.
-template <int ACT, int TPR, int NV>
+// WHOLE: K is a multiple of 8, so a row is whole vectors, all of them loaded
+// before the first is looked at; past the row the resource ends: zeros.
+template <int ACT, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(RowsArgs a)
 {
     constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;  // rows a workgroup
     const int tid = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+    const int64_t row = (int64_t)blockIdx.x * RPW + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     if (row >= a.B)
         return;  // whole waves
     const int64_t base = row * a.K;
     float v[NV][RQ_V];
-    uint32_t top = 0;  // largest |x| as bits: infinities and NaNs above all finite values
+    if constexpr (WHOLE) {
+        Raw8<ACT> raw[NV];
+        const __amdgpu_buffer_rsrc_t xr =
+            make_rsrc((const uint8_t *)a.x + base * Raw8<ACT>::ESZ, a.K * Raw8<ACT>::ESZ);
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
-        const int64_t k = ((int64_t)j * TPR + tid) * RQ_V;
-        load8<ACT>(a.x, base + k, a.K - k, v[j]);
+        for (int j = 0; j < NV; j++)
+            raw[j].load(xr, (j * TPR + tid) * RQ_V * Raw8<ACT>::ESZ);
+#pragma unroll
+        for (int j = 0; j < NV; j++)
+            raw[j].floats(v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            const int64_t k = ((int64_t)j * TPR + tid) * RQ_V;
+            if (j == 0 || (int64_t)j * TPR * RQ_V < a.K)  // uniform
+                load8<ACT>(a.x, base + k, a.K - k, v[j]);
+            else
+#pragma unroll
+                for (int i = 0; i < RQ_V; i++)
+                    v[j][i] = 0.f;
+        }
     }
+    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < NV; j++)
-#pragma unroll
-        for (int i = 0; i < RQ_V; i++)
-            top = max(top, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+        top = top8(v[j], top);
     for (int64_t k = ((int64_t)NV * TPR + tid) * RQ_V; k < a.K; k += TPR * RQ_V) {
         float w[RQ_V];
         load8<ACT>(a.x, base + k, a.K - k, w);
-#pragma unroll
-        for (int i = 0; i < RQ_V; i++)
-            top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
+        top = top8(w, top);
     }
-    for (int d = 32; d; d >>= 1)
-        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    top = wave_max(top);
     if constexpr (TPR > 64) {
         __shared__ uint32_t tops[TPR / 64];
         if ((threadIdx.x & 63) == 0)
@@ -106,16 +65,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(Ro
         for (int w = 0; w < TPR / 64; w++)
             top = max(top, tops[w]);
     }
-    const bool bad = top >= 0x7F800000u;
-    const float s = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 127.f;
-    const bool zero = bad || s == 0.f;
-    const float inv = zero ? 0.f : 1.f / s;
+    const RowScale sc(top);
 
     // the registers' codes once, then to every row they go to
     u32x2 c[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++)
-        c[j] = zero ? u32x2{0u, 0u} : pack_codes8(v[j], s, inv);
+        c[j] = sc.codes(v[j]);
     const int reps = a.pos ? a.topk : 1;
     for (int r = 0; r < reps; r++) {
         int64_t to = row;
@@ -131,7 +87,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(Ro
         }
         int8_t *o = a.codes + to * a.ldc;
         if (tid == 0)
-            a.scales[to] = s;
+            a.scales[to] = sc.s;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             const int64_t k = ((int64_t)j * TPR + tid) * RQ_V;
@@ -141,7 +97,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(Ro
         for (int64_t k = ((int64_t)NV * TPR + tid) * RQ_V; k < a.ldc; k += TPR * RQ_V) {
             float w[RQ_V];
             load8<ACT>(a.x, base + k, a.K - k, w);
-            *(u32x2 *)(o + k) = zero ? u32x2{0u, 0u} : pack_codes8(w, s, inv);
+            *(u32x2 *)(o + k) = sc.codes(w);
         }
     }
 }
@@ -151,10 +107,15 @@ static void rows_go(bool f32, const RowsArgs &a, hipStream_t st)
 {
     constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
     const dim3 g((unsigned)((a.B + RPW - 1) / RPW)), blk(TPR > 256 ? TPR : 256);
-    if (f32)
-        hipLaunchKernelGGL((quantize_rows_kernel<ACT_F32, TPR, NV>), g, blk, 0, st, a);
+    const bool whole = a.K % RQ_V == 0;
+    if (f32 && whole)
+        hipLaunchKernelGGL((quantize_rows_kernel<ACT_F32, TPR, NV, true>), g, blk, 0, st, a);
+    else if (f32)
+        hipLaunchKernelGGL((quantize_rows_kernel<ACT_F32, TPR, NV, false>), g, blk, 0, st, a);
+    else if (whole)
+        hipLaunchKernelGGL((quantize_rows_kernel<ACT_BF16, TPR, NV, true>), g, blk, 0, st, a);
     else
-        hipLaunchKernelGGL((quantize_rows_kernel<ACT_BF16, TPR, NV>), g, blk, 0, st, a);
+        hipLaunchKernelGGL((quantize_rows_kernel<ACT_BF16, TPR, NV, false>), g, blk, 0, st, a);
 }
 
 // As few threads a row as hold it in registers; long rows of which there are not

@@ -9,7 +9,7 @@
 // 64-byte halves of a cache line) and keep SLOTS such pairs in flight in
 // registers.  The waves' int32 sums meet in LDS: sums of whole numbers, so the
 // split changes no bit.  A lane ends with four neighbouring channels of one row.
-#include "int8.h"
+#include "int8_quant.h"
 
 namespace qg {
 
@@ -29,9 +29,18 @@ __device__ __forceinline__ int sm_tile(const I8Args &a, int g, int r)
     }
 }
 
-template <int R, int SLOTS, bool DUAL, int OUTT>
-__global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
+// FUSED: up to SM_FUSED_B rows come as floats of type ACT (xf), which every
+// workgroup quantises for itself into LDS while its first weights are on their
+// way: a row is 10 KB to read from L2, a launch of its own costs more (1 x 5120 x
+// 5120: 10.0 us in two launches, 6.9 in one).  Rows longer than SM_FUSED_BYTES
+// in all would take the registers that let two workgroups share a CU (20 us).
+constexpr int SM_FUSED_B = 2, SM_FUSED_BYTES = 8 * 1024, SM_FUSED_NV = SM_FUSED_BYTES / (64 * SM_W * RQ_V);
+
+template <int R, int SLOTS, bool DUAL, int OUTT, bool FUSED, int ACT>
+__global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a, const void *xf)
 {
+    __shared__ uint8_t xq[FUSED ? SM_FUSED_BYTES : 16];  // [rows][64 S] codes
+    __shared__ uint32_t tops[SM_W];
     __shared__ i32x4 red[SM_W * R * 64];
     const int g = blockIdx.x, row0 = blockIdx.y * 16;
     const int rows = min(16, a.B - row0);
@@ -54,7 +63,21 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
     // The i'th pair of slabs of this wave (S is even) into a slot; past the
     // last one zeros from empty resources, so that every step issues the same
     // loads and the waits for the slots are exact.
-    i32x4 wv[SLOTS][2][R], xv[SLOTS][2];
+    i32x4 wv[SLOTS][2][R], xv[FUSED ? 1 : SLOTS][2];
+    // FUSED: all threads on one row, or half of them on each of two
+    const int tpr = rows == 2 ? 32 * SM_W : 64 * SM_W, xr_ = rows == 2 ? threadIdx.x / tpr : 0;
+    const int tt = threadIdx.x - xr_ * tpr, kp = a.S * 64;
+    Raw8<ACT> fv[FUSED ? SM_FUSED_NV : 1];  // K is a multiple of 8
+    if constexpr (FUSED) {                  // before the weights: loads come back in order
+        constexpr int ESZ = Raw8<ACT>::ESZ;
+        const __amdgpu_buffer_rsrc_t fr = make_rsrc(xf, (int64_t)rows * a.K * ESZ);
+#pragma unroll
+        for (int j = 0; j < SM_FUSED_NV; j++) {
+            const int k = (j * tpr + tt) * RQ_V;  // past the row: past the resource, zeros
+            fv[j].load(fr, k < a.K ? (xr_ * a.K + k) * ESZ : 0x7FFFFF00);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
     auto load = [&](int i, int slot) {
         const int s = (i * SM_W + wid) * 2;
         const bool live = s < a.S;
@@ -65,7 +88,8 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
             for (int r = 0; r < R; r++)
                 wv[slot][h][r] = __builtin_bit_cast(
                     i32x4, bload16_nt(make_rsrc(wt[r], live ? tile_bytes : 0), lane * 16, live ? (s + h) << 10 : 0));
-            xv[slot][h] = __builtin_bit_cast(i32x4, bload16(xr, xo + ((s + h) << 6), 0));
+            if constexpr (!FUSED)
+                xv[slot][h] = __builtin_bit_cast(i32x4, bload16(xr, xo + ((s + h) << 6), 0));
         }
     };
     const int n = (a.S / 2 + SM_W - 1) / SM_W;
@@ -74,17 +98,59 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
         load(u, u);
         __builtin_amdgcn_sched_barrier(0);  // in the order of the loop
     }
-    auto multiply = [&](int u) {
+    [[maybe_unused]] float own_scale = 0.f;
+    if constexpr (FUSED) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int j = 0; j < SM_FUSED_NV; j++) {
+            float v[RQ_V];
+            fv[j].floats(v);
+            top = top8(v, top);
+        }
+        top = wave_max(top);
+        if (lane == 0)
+            tops[wid] = top;
+        __syncthreads();
+        uint32_t top0 = 0, top1 = 0;
+#pragma unroll
+        for (int k = 0; k < SM_W / 2; k++) {
+            top0 = max(top0, tops[k]);
+            top1 = max(top1, tops[SM_W / 2 + k]);
+        }
+        if (rows == 1)
+            top0 = max(top0, top1);
+        const RowScale sc(xr_ ? top1 : top0);
+        own_scale = RowScale(c16 ? top1 : top0).s;  // of the row that this lane stores
+#pragma unroll
+        for (int j = 0; j < SM_FUSED_NV; j++) {
+            const int k = (j * tpr + tt) * RQ_V;
+            if (k < kp) {  // with the padding's zeros
+                float v[RQ_V];
+                fv[j].floats(v);
+                *(u32x2 *)(xq + xr_ * kp + k) = sc.codes(v);
+            }
+        }
+        __syncthreads();
+    }
+    auto multiply = [&](int i, int u) {  // the i'th pair, in slot u
+        const int s = (i * SM_W + wid) * 2;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            i32x4 x;
+            if constexpr (FUSED)
+                x = *(const i32x4 *)(xq + (c16 < rows ? c16 * kp : 0) + (s < a.S ? (s + h) << 6 : 0) + kg * 16);
+            else
+                x = xv[u][h];
 #pragma unroll
             for (int r = 0; r < R; r++)
-                acc[r] = mfma_i8(wv[u][h][r], xv[u][h], acc[r]);
+                acc[r] = mfma_i8(wv[u][h][r], x, acc[r]);
+        }
     };
-    for (int i = SLOTS; i < n; i += SLOTS) {
+    int i = SLOTS;
+    for (; i < n; i += SLOTS) {
 #pragma unroll
         for (int u = 0; u < SLOTS; u++) {
-            multiply(u);
+            multiply(i - SLOTS + u, u);
             __builtin_amdgcn_sched_barrier(0);
             load(i + u, u);
             __builtin_amdgcn_sched_barrier(0);
@@ -92,7 +158,7 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
     }
 #pragma unroll
     for (int u = 0; u < SLOTS; u++)
-        multiply(u);
+        multiply(i - SLOTS + u, u);
 
 #pragma unroll
     for (int r = 0; r < R; r++)
@@ -114,7 +180,7 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
         if constexpr (DUAL)
             up = sum(wid + RO);
         if (c16 < rows && n < a.ncols) {
-            const float xs = a.xs[row0 + c16];
+            const float xs = FUSED ? own_scale : a.xs[row0 + c16];
             const f32x4 t = *(const f32x4 *)(ws + n);
             f32x4 out;
 #pragma unroll
@@ -132,15 +198,26 @@ __global__ __launch_bounds__(64 * SM_W, 2) void i8_small_kernel(I8Args a)
     }
 }
 
-template <int R, int SLOTS, bool DUAL>
-static void small_go(const I8Args &a, int outt, hipStream_t st)
+template <int R, int SLOTS, bool DUAL, bool FUSED, int ACT>
+static void small_go(const I8Args &a, const void *xf, int outt, hipStream_t st)
 {
     const int groups = DUAL ? a.Nh / 16 : (a.RT + R - 1) / R;
     const dim3 grid((unsigned)groups, (unsigned)((a.B + 15) / 16)), blk(64 * SM_W);
     if (outt == OUT_F32)
-        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_F32>), grid, blk, 0, st, a);
+        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_F32, FUSED, ACT>), grid, blk, 0, st, a, xf);
     else
-        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_BF16>), grid, blk, 0, st, a);
+        hipLaunchKernelGGL((i8_small_kernel<R, SLOTS, DUAL, OUT_BF16, FUSED, ACT>), grid, blk, 0, st, a, xf);
+}
+
+template <bool FUSED, int ACT>
+static void small_shape(const I8Args &a, const void *xf, int outt, hipStream_t st)
+{
+    if (a.Nh)
+        small_go<2, 4, true, FUSED, ACT>(a, xf, outt, st);
+    else if (a.N >= 8192)
+        small_go<2, 4, false, FUSED, ACT>(a, xf, outt, st);
+    else
+        small_go<1, 5, false, FUSED, ACT>(a, xf, outt, st);
 }
 
 // Up to two rows any weight, up to 16 rows one of 8192 channels or more.
@@ -151,12 +228,21 @@ bool i8_small_wins(int64_t B, int64_t N) { return B <= 2 || (B <= 16 && N >= 819
 
 hipError_t launch_i8_small(const I8Args &a, int outt, hipStream_t st)
 {
-    if (a.Nh)
-        small_go<2, 4, true>(a, outt, st);
-    else if (a.N >= 8192)
-        small_go<2, 4, false>(a, outt, st);
+    small_shape<false, ACT_F32>(a, nullptr, outt, st);
+    return hipGetLastError();
+}
+
+bool i8_small_fuses(int64_t B, int64_t K, int64_t S)
+{
+    return B <= SM_FUSED_B && K % RQ_V == 0 && B * S * 64 <= SM_FUSED_BYTES;
+}
+
+hipError_t launch_i8_small_fused(const I8Args &a, const void *x, int act, int outt, hipStream_t st)
+{
+    if (act == QGEMM_F32)
+        small_shape<true, ACT_F32>(a, x, outt, st);
     else
-        small_go<1, 5, false>(a, outt, st);
+        small_shape<true, ACT_BF16>(a, x, outt, st);
     return hipGetLastError();
 }
 

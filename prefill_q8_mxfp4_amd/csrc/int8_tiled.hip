@@ -536,15 +536,19 @@ __global__ __launch_bounds__(64) void i8_tiled_reduce_kernel(I8Args a, int mtile
 // with its weight tiles; a workgroup finds its expert by a scan of the experts'
 // row-tile counts, and those past the real count leave.  Row tiles are dealt to
 // the XCDs in turn (the real ones are the first of the bound, so runs of them
-// would leave half of the XCDs idle), a row tile's weight tiles to one XCD.
+// would leave half of the XCDs idle), a row tile's weight tiles to one XCD, `per`
+// of them to a workgroup.
 template <typename S, bool DUAL, int OUTT>
-__global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8Groups grp, int ntiles)
+__global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8Groups grp, int ntiles,
+                                                                     int per)
 {
     __shared__ int wsum[S::NW], found[4];
     constexpr int NT = 64 * S::NW;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int loc = blockIdx.x / 8;
-    const int mt = loc / ntiles * 8 + blockIdx.x % 8, nt = loc % ntiles;  // row tile over all experts
+    const int groups = (ntiles + per - 1) / per;
+    const int mt = loc / groups * 8 + blockIdx.x % 8;  // row tile over all experts
+    const int nt0 = loc % groups * per;
     // PER neighbouring experts a thread: up to NT * PER of them with one wait for
     // their offsets
     constexpr int PER = 4;
@@ -601,10 +605,16 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
     const int row0 = __builtin_amdgcn_readfirstlane(found[1]);
     const int rows = min(S::BM, __builtin_amdgcn_readfirstlane(found[2]) - row0);
     const uint8_t *w = uniform_ptr(grp.wtab[e]);
-    i32x4 acc[S::TM][S::TN];
-    const TiScales<S, DUAL> sc(a, w, row0, rows, nt);
-    TI_SUMS(S, DUAL, a, w, row0, rows, nt, 0, a.S)
-    ti_finish<S, DUAL, OUTT>(a, sc, row0, rows, nt, own, acc);
+    TI_LDS(S, lds);
+    for (int nt = nt0; nt < min(nt0 + per, ntiles); nt++) {
+        if (nt > nt0)
+            __syncthreads();  // every wave is done with its outputs' LDS
+        i32x4 acc[S::TM][S::TN];
+        const TiScales<S, DUAL> sc(a, w, row0, rows, nt);
+        ti_tile_sums<S, DUAL>(a, w, row0, rows, nt, 0, a.S, lds, acc);
+        ti_finish<S, DUAL, OUTT>(a, sc, row0, rows, nt,
+                                 ti_own<S>(lds, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), acc);
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -753,15 +763,20 @@ static void grouped_go(const I8Args &a, const I8Groups &g, int outt, hipStream_t
     const int ntiles = (cols + S::BN - 1) / S::BN;
     // an expert adds at most one partial tile, and at most B experts have rows
     const int64_t tiles = a.B / S::BM + (g.E < a.B ? g.E : a.B);
-    const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * ntiles)), blk(64 * S::NW);
+    // Two weight tiles a workgroup where a tile is little work, so that finding
+    // the expert and its weights is less of it: one against two, 20480 rows over
+    // 512 experts of 2048 x 512 125 against 107 us, 160 rows of 1024 x 2048 40.5
+    // against 38; four leave the rounds uneven (51).
+    const int per = S::BM == 32 || a.S <= 16 ? 2 : 1, groups = (ntiles + per - 1) / per;
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * groups)), blk(64 * S::NW);
     if (a.Nh && outt == OUT_F32)
-        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_F32>), grid, blk, 0, st, a, g, ntiles, per);
     else if (a.Nh)
-        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, true, OUT_BF16>), grid, blk, 0, st, a, g, ntiles, per);
     else if (outt == OUT_F32)
-        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_F32>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_F32>), grid, blk, 0, st, a, g, ntiles, per);
     else
-        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_BF16>), grid, blk, 0, st, a, g, ntiles);
+        hipLaunchKernelGGL((i8_grouped_kernel<S, false, OUT_BF16>), grid, blk, 0, st, a, g, ntiles, per);
 }
 
 // Rows of a tile by the mean rows of an expert.  Measured with 128 experts of

@@ -82,7 +82,8 @@ def quantize_ref(x, ldc):
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("B,K", [(1, 1), (3, 7), (5, 16), (130, 63), (7, 512), (4, 1023), (4, 1024), (6, 1025), (2, 2729),
-                                 (3, 8192), (3, 8200), (2, 18432), (2, 18433), (1, 40001), (1000, 256)])
+                                 (3, 8192), (3, 8200), (2, 18432), (2, 18433), (1, 40001), (1000, 256), (300, 2500),
+                                 (4096, 512), (4101, 509), (5000, 1)])
 def test_quantize_rows(act, B, K):
     g = gen(B * 7919 + K)
     x = torch.randn(B, K, generator=g) * torch.exp(torch.randn(B, 1, generator=g))
@@ -222,7 +223,9 @@ def test_product_swiglu(B, nh, K, out):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
-@pytest.mark.parametrize("B,N,K", [(1, 64, 100), (70, 272, 1000), (300, 513, 640)])
+@pytest.mark.parametrize("B,N,K", [(1, 64, 100), (1, 50, 1), (2, 37, 2048), (2, 33, 4096), (2, 33, 4104), (2, 33, 1001),
+                                   (1, 8200, 328), (1, 8200, 333),
+                                   (1, 20, 8192), (1, 20, 8200), (2, 9000, 96), (70, 272, 1000), (300, 513, 640)])
 def test_product_of_float_rows(B, N, K, act):
     """run() quantises as quantize_rows does: the same bits as run_codes of its
     codes, by the workspace and by the library's own scratch."""
