@@ -120,7 +120,10 @@ typedef enum qgemm_tier {
                               order per output across the tier, so a batch
                               row's result does not depend on B there */
     QGEMM_TIER_TILED = 2,  /* batch x weight tiles staged through LDS; for large B
-                              (above the small-batch limits) */
+                              (above the small-batch limits).  QGEMM_INT8 weights
+                              go here from B = 3, or from B = 17 when N >= 8192,
+                              and to the small-batch tier below; both give the
+                              same bits */
     QGEMM_TIER_GEMV = 3    /* B = 1, 2: one workgroup per 16-row tile over all of
                               K, fp32 FMA on the vector ALUs, a fixed-order
                               cross-lane sum; no K split and no workspace.
@@ -374,8 +377,9 @@ int qgemm_run_codes(const qgemm_plan *plan, int64_t B, const void *w, const int8
  * neither read nor written (qgemm_route leaves such rows when it drops
  * choices).  An expert whose own two offsets are out of order or outside 0..T
  * is left out and sets QGEMM_DEV_BAD_OFFSETS; y is then not to be trusted.
- * qgemm_grouped_tier tells the route; each expert's rows are bitwise those of
- * qgemm_run_codes on them, on either. */
+ * One route (qgemm_grouped_tier: QGEMM_TIER_TILED), whose tiles are as high as
+ * the mean expert has rows; each expert's rows are bitwise those of
+ * qgemm_run_codes on them. */
 int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const void *const *w_table,
                             const int32_t *offsets, const int8_t *codes, int64_t ldc, const float *scales, void *y,
                             void *stream);

@@ -936,12 +936,17 @@ static int check_run(const qgemm_plan *plan, int64_t B, const void *w, const voi
     return QGEMM_OK;
 }
 
+// A launch's threads are counted in 32 bits.
+static const int64_t MAX_THREADS = (1ll << 32) - 1;
+
 // The INT8 product of B > 0 rows of codes; `part` (part_bytes) holds the
 // partial tiles of a K split, or null.
 static int i8_product(const qgemm_plan *plan, const I8Args &a, uint8_t *part, int64_t part_bytes, hipStream_t st)
 {
     hipError_t e;
     if (i8_tier(plan, a.B) == QGEMM_TIER_SKINNY) {
+        if (a.B > 16 * 65535)
+            return fail(QGEMM_EINVAL, "qgemm_run: B=%d exceeds the small-batch tier's grid", a.B);
         e = launch_i8_small(a, plan->p.out, st);
     } else {
         I8TiCfg c = i8_tiled_cfg(a, part != nullptr, plan->p.kn.i8_shape, plan->p.kn.ti_split);
@@ -1255,7 +1260,7 @@ int qgemm_dequantize(qgemm_format fmt, const void *w, float *w_out, int64_t N, i
     a.RT = (int)L.RT;
     a.scale_off = L.scale_off;
     a.meta_off = L.meta_off;
-    if (fmt == QGEMM_INT8 && L.RT * L.S * 64 > 0x7FFFFFFFll * 256)
+    if (fmt == QGEMM_INT8 && L.RT * L.S * 64 + 256 > MAX_THREADS)
         return fail(QGEMM_EINVAL, "qgemm_dequantize: too large");
     hipError_t e0 = launch_dequant((int)fmt, a, w_out, (hipStream_t)stream);
     if (e0 != hipSuccess)
@@ -1286,7 +1291,7 @@ int qgemm_pack_device(qgemm_format fmt, int64_t N, int64_t K, const void *codes,
     if (out_bytes < (size_t)L.total)
         return fail(QGEMM_EINVAL, "qgemm_pack_device: output buffer %zu bytes < %lld needed", out_bytes,
                     (long long)L.total);
-    if (L.total / 16 > 0x7FFFFFFFll * 256)
+    if (L.total / 16 + 256 > MAX_THREADS)
         return fail(QGEMM_EINVAL, "qgemm_pack_device: too large");
     const hipError_t e = launch_i8_pack(L, (const int8_t *)codes, (const float *)scales, (uint8_t *)out,
                                         (hipStream_t)stream);
@@ -1310,6 +1315,9 @@ static int check_rows(const char *who, qgemm_dtype act, int64_t B, int64_t K, co
         return fail(QGEMM_EINVAL, "%s: null pointer", who);
     if (!aligned16(x) || !aligned16(codes) || ((uintptr_t)scales & 3u))
         return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
+    if ((B + 3) * (K <= 1024 ? 64 : K <= 2048 || B > 256 ? 256 : 1024) > MAX_THREADS)
+        return fail(QGEMM_EINVAL, "%s: B=%lld rows of K=%lld are too many for one launch", who, (long long)B,
+                    (long long)K);
     return QGEMM_OK;
 }
 
@@ -1393,8 +1401,8 @@ int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const 
     const I8Args a = i8_args(plan->p, T, nullptr, codes, ldc, scales, y);
     const int forced = plan->p.kn.i8_shape;
     const int shape = forced == I8_64x128 || forced >= I8_32x128 ? forced : i8_grouped_shape(E, T);
-    // row tiles of 32 at least, weight tiles of 128
-    if ((T / 32 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 8 + 1) > 0x7FFFFFFFll)
+    // row tiles of 32 at least, weight tiles of 128, 512 threads at most
+    if ((T / 32 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 8 + 1) > MAX_THREADS / 512)
         return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: grid too large");
     const hipError_t e = launch_i8_grouped(a, g, shape, plan->p.out, (hipStream_t)stream);
     return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run_grouped_codes: kernel launch");
@@ -1431,6 +1439,11 @@ static int check_moves(const char *who, qgemm_dtype dt, int64_t T, int64_t topk,
     if (H < 1 || H > (1ll << 20) || R < 0 || R > (1ll << 30))
         return fail(QGEMM_EINVAL, "%s: H=%lld outside 1..2^20 or R=%lld outside 0..2^30", who, (long long)H,
                     (long long)R);
+    // a wave a choice, or a wave 1 KB of a token's row
+    const int64_t waves = T * (H / (dt == QGEMM_F32 ? 256 : 512) + 1);
+    if ((T * topk + 3) * 64 > MAX_THREADS || (waves + 3) * 64 > MAX_THREADS)
+        return fail(QGEMM_EINVAL, "%s: T=%lld tokens of topk=%lld choices and H=%lld are too many for one launch", who,
+                    (long long)T, (long long)topk, (long long)H);
     return QGEMM_OK;
 }
 

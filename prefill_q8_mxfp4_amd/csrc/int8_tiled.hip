@@ -596,8 +596,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
             first += cnt[k];
         }
         __syncthreads();
-        if (found[0] >= 0)
-            break;  // uniform
+        if (found[0] >= 0 && blockIdx.x)
+            break;  // uniform; the first workgroup looks at every expert's offsets
     }
     const int e = __builtin_amdgcn_readfirstlane(found[0]);
     if (e < 0)

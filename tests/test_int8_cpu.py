@@ -111,6 +111,9 @@ def test_run_refusals():
         assert but(4, ldc) == q.EINVAL, ldc
     assert but(1, -1) == q.EINVAL and but(1, (1 << 30) + 1) == q.EINVAL
     assert but(1, 1 << 22) == q.EINVAL                          # 2^31 bytes of codes
+    st, small = _create(4, 1, 1, 0, 2, 16, 16, 1)               # forced to the small-batch tier
+    assert codes(small, 16 * 65535 + 1, P16, P16, 16, P16, P16, None, 0, None) == q.EINVAL
+    L.qgemm_destroy(small)
     assert but(7, P16 + 128) == q.EINVAL                        # workspace alignment
     L.qgemm_destroy(h)
     st, h = _create(0, 0, 0, 0, 0, 256, 512, 0)
@@ -149,6 +152,7 @@ def test_row_refusals():
 
     assert L.qgemm_quantize_rows(1, 0, 512, None, None, 512, None, None) == q.OK
     assert but(0, 2) == q.EINVAL and but(1, -1) == q.EINVAL and but(2, 0) == q.EINVAL
+    assert but(1, 1 << 26) == q.EINVAL                          # threads of one launch
     assert but(2, (1 << 20) + 1) == q.EINVAL and but(5, 510) == q.EINVAL and but(5, 496) == q.EINVAL
     for i in (3, 4, 6):
         assert but(i, None) == q.EINVAL, i
@@ -204,6 +208,7 @@ def test_move_refusals(name):
     assert but(0, 2) == q.EINVAL
     for i, v in ((1, -1), (1, (1 << 30) + 1), (2, 0), (2, 65), (3, 0), (3, (1 << 20) + 1), (4, -1), (4, (1 << 30) + 1)):
         assert but(i, v) == q.EINVAL, (i, v)
+    assert but(1, 1 << 26) == q.EINVAL                          # threads of one launch
     for i in pointers:
         assert but(i, None) == q.EINVAL, i
         assert but(i, P16 + 2) == q.EINVAL, i

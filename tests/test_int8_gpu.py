@@ -340,6 +340,11 @@ def test_experts_bad_offsets(shape, monkeypatch):
         y = torch.full((T, N), 7.0, device=DEV)
         plan.run_grouped_codes(dx, dsx, table, torch.tensor(off, dtype=torch.int32, device=DEV), y)
         assert q.device_status(clear=True) == q.DEV_BAD_OFFSETS, off
+    many = torch.full((3001,), 40, dtype=torch.int32)   # expert 0 has all rows, a late one breaks the rules
+    many[0], many[2500] = 0, 39
+    y = torch.full((T, N), 7.0, device=DEV)
+    plan.run_grouped_codes(dx, dsx, table[:1].expand(3000).contiguous(), many.to(DEV), y)
+    assert q.device_status(clear=True) == q.DEV_BAD_OFFSETS
     y = torch.full((T, N), 7.0, device=DEV)
     plan.run_grouped_codes(dx, dsx, table, torch.zeros(E + 1, dtype=torch.int32, device=DEV), y)
     assert q.device_status() == 0 and (y == 7.0).all()
