@@ -107,7 +107,7 @@ hipError_t launch_i8_small_fused(const I8Args &a, const void *x, int act, int ou
 
 // ---- int8_tiled.hip: many rows, tiles through LDS
 enum I8Shape {  // batch rows x channels of a tile
-    I8_32x32 = 1, I8_32x64, I8_64x64, I8_64x128, I8_128x128R, I8_128x256, I8_256x256,
+    I8_32x32 = 1, I8_32x64, I8_64x64, I8_64x128, I8_64x128R, I8_128x128R, I8_128x256, I8_256x256,
     I8_32x128, I8_128x128,  // routed rows (and 64 x 128)
 };
 struct I8TiCfg {

@@ -44,6 +44,7 @@ using T32x32 = TiShape<2, 1, 1, 2, 8>;
 using T32x64 = TiShape<2, 2, 1, 2, 8>;
 using T64x64 = TiShape<2, 2, 2, 2, 8>;
 using T64x128 = TiShape<2, 2, 2, 4>;
+using T64x128R = TiShape<2, 4, 2, 2, 4>;
 using T128x128R = TiShape<2, 4, 4, 2, 4>;
 using T128x256 = TiShape<2, 4, 4, 4>;
 using T256x256 = TiShape<2, 4, 8, 4>;
@@ -626,7 +627,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
 // L2 and of the clock: step[0] with up to 128 of them, step[1] with 256, step[2]
 // with all that the CUs hold.  Choices it makes, with the runner-up: 16 x 5120 x
 // 5120 32x32 7.8 (32x64 8.5); 70 x 5120 x 17408 32x64 28 (64x64 31); 128 x 5120 x
-// 5120 64x64 11.7 (32x64 15.7); 512 x 5120 x 5120 128x128R 21 (64x128 24); 1024:
+// 5120 64x64 11.7 (64x128R 14.0); 256: 64x128R 14.7 (64x64 20); 512: 128x128R 21 (64x128 24); 1024:
 // 128x256 32 (64x128 39); 2048: 256x256 55 (128x128R 66).
 struct ShapeCost {
     int BM, BN, resident;  // workgroups a CU holds
@@ -638,6 +639,7 @@ static const ShapeCost COST[] = {
     {32, 64, 1, 0.3f, {0.085f, 0.092f, 0.092f}},    // I8_32x64
     {64, 64, 1, 0.8f, {0.103f, 0.112f, 0.112f}},    // I8_64x64
     {64, 128, 3, 1.0f, {0.225f, 0.250f, 0.520f}},   // I8_64x128
+    {64, 128, 1, 0.5f, {0.145f, 0.165f, 0.165f}},   // I8_64x128R
     {128, 128, 1, 1.0f, {0.200f, 0.280f, 0.280f}},  // I8_128x128R
     {128, 256, 1, 2.0f, {0.300f, 0.520f, 0.520f}},  // I8_128x256
     {256, 256, 1, 5.0f, {0.540f, 0.820f, 0.820f}},  // I8_256x256
@@ -733,6 +735,7 @@ static void tiled_shape(const I8Args &a, const I8TiCfg &c, int32_t *part, hipStr
     case I8_32x64: tiled_go<T32x64, DUAL, OUTT>(a, c, part, st); break;
     case I8_64x64: tiled_go<T64x64, DUAL, OUTT>(a, c, part, st); break;
     case I8_64x128: tiled_go<T64x128, DUAL, OUTT>(a, c, part, st); break;
+    case I8_64x128R: tiled_go<T64x128R, DUAL, OUTT>(a, c, part, st); break;
     case I8_128x128R: tiled_go<T128x128R, DUAL, OUTT>(a, c, part, st); break;
     case I8_128x256: tiled_go<T128x256, DUAL, OUTT>(a, c, part, st); break;
     default:

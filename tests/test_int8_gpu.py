@@ -161,7 +161,7 @@ def test_product(B, N, K, out):
             assert torch.equal(y, first), (tier, ws)
 
 
-@pytest.mark.parametrize("shape", range(1, 8))
+@pytest.mark.parametrize("shape", range(1, 9))
 @pytest.mark.parametrize("B,N,K", [(5, 70, 200), (130, 300, 700), (300, 544, 2100)])
 def test_product_tile_shapes(B, N, K, shape, monkeypatch):
     """Every tile shape of the large-batch tier, its K in one, two and five
@@ -193,7 +193,7 @@ def test_product_last_round_in_pieces(B, N, K, swiglu, monkeypatch):
     cw = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int64).to(torch.int8).to(DEV)
     w = q.pack_int8(cw, torch.rand(N, generator=g).to(DEV))
     epi, cols = ("swiglu", N // 2) if swiglu else ("none", N)
-    monkeypatch.setenv("QGEMM_I8_SHAPE", "7")
+    monkeypatch.setenv("QGEMM_I8_SHAPE", "8")
     ys = [q.Plan("int8", N, K, act="bf16", out="bf16", epilogue=epi, tier=t).run_codes(
         dx, dsx, w, torch.full((B, cols), float("nan"), dtype=torch.bfloat16, device=DEV))
         for t in ("skinny", "tiled")]
@@ -304,7 +304,7 @@ def test_experts(counts, N, K, behind, swiglu, monkeypatch):
     off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
     epi, ncols = ("swiglu", N // 2) if swiglu else ("none", N)
     for out in ("f32", "bf16"):
-        for tier in (None, 4, 8, 9):      # by the mean count, and each of its tile shapes
+        for tier in (None, 4, 9, 10):      # by the mean count, and each of its tile shapes
             if tier is not None:
                 monkeypatch.setenv("QGEMM_I8_SHAPE", str(tier))
             plan = q.Plan("int8", N, K, act="bf16", out=out, epilogue=epi)
@@ -325,7 +325,7 @@ def test_experts(counts, N, K, behind, swiglu, monkeypatch):
     assert q.device_status() & q.DEV_BAD_OFFSETS == 0
 
 
-@pytest.mark.parametrize("shape", [4, 8, 9])
+@pytest.mark.parametrize("shape", [4, 9, 10])
 def test_experts_bad_offsets(shape, monkeypatch):
     """An expert whose offsets break the rules is left out and reported."""
     N, K, T, E = 64, 128, 40, 4
