@@ -229,7 +229,12 @@ struct TiLds {
     __shared__ __attribute__((aligned(1024))) uint8_t ldw2[S::WST], ldw3[S::WST];         \
     const TiLds L = {{ldx0, ldx1}, {ldw0, ldw1, ldw2, ldw3}}
 
-__device__ __forceinline__ int x_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// Rows 2 m and 2 m + 1 take m: then the pieces of one k group of 16 rows lie in 16
+// different 16-byte bank groups, and so do those of rows 0-3 and 12-15 of one k
+// group with rows 4-11 of the next, which a 16-byte read takes together.
+// (r & 7 with r's bit 3 flipping the lowest does only the first: 39 % of the LDS
+// cycles were conflicts.)
+__device__ __forceinline__ int x_swizzle(int r) { return (r >> 1) & 7; }
 
 // What a wave loads of a tile: KBs of codes (rows past the last are copies of it)
 // and weight tiles; steps from `end` on come from an empty resource.
@@ -692,7 +697,7 @@ I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int shape, int pieces)
             else if (rest)
                 us += round_us(p, rest, 4 * per);
             if (c.split > 1)  // a second launch, and the partial tiles written and read
-                us += 3.f + 0.5e-6f * (float)c.part_bytes;
+                us += 4.f + 0.5e-6f * (float)c.part_bytes;
             if (us < best_us) {
                 best_us = us;
                 best = c;
