@@ -120,7 +120,7 @@ static void rows_go(bool f32, const RowsArgs &a, hipStream_t st)
 
 // As few threads a row as hold it in registers; long rows of which there are not
 // enough for the chip get four times as many (70 rows of 17408 floats: 6.6 us
-// with 256 threads, 5.0 with 1024).
+// with 256 threads, 6.0 with 1024).
 hipError_t launch_quantize_rows(int act, const RowsArgs &a, hipStream_t st)
 {
     const bool f32 = act == QGEMM_F32;
