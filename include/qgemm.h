@@ -391,7 +391,8 @@ int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const 
  * expert held elsewhere, a padding token): it has no row, counts nothing and
  * gets no gradient.  The same expert may be chosen twice.  Rows are row-major
  * without gaps, QGEMM_F32 or QGEMM_BF16, 16-byte aligned; inputs and outputs
- * must not overlap.  T = 0 is a no-op (qgemm_route then writes zero offsets).
+ * must not overlap.  Positions are those of qgemm_route: where two choices name
+ * one row, either's is written.  T = 0 is a no-op (qgemm_route then writes zero offsets).
  * Results are deterministic. */
 #define QGEMM_MAX_TOPK 64
 

@@ -208,7 +208,7 @@ def pack_int8(codes, scales, out=None, stream=None):
 def quantize_rows(x, codes=None, scales=None, stream=None):
     """qgemm_quantize_rows: float32 or bfloat16 rows x [B][K] to int8 codes
     [B][K] (at a pitch of code_stride(K)) and float32 scales [B]; outputs are
-    allocated unless given."""
+    allocated unless given.  Codes at a larger pitch get zeros up to it."""
     dt = _dtype(x, "x")
     B, K = _rows(x, "x")
     if codes is None:

@@ -939,6 +939,20 @@ static int check_run(const qgemm_plan *plan, int64_t B, const void *w, const voi
 // A launch's threads are counted in 32 bits.
 static const int64_t MAX_THREADS = (1ll << 32) - 1;
 
+// Rows that one launch of the quantisation does not take.
+static bool too_many_rows(int64_t B, int64_t K)
+{
+    return (B + 3) * (K <= 1024 ? 64 : K <= 2048 || B > 256 ? 256 : 1024) > MAX_THREADS;
+}
+
+// An INT8 call that no launch takes: codes or outputs that 32-bit counts do not
+// reach, or channels whose workgroups (512 threads a row tile) would not fit.
+static bool i8_too_large(const Problem &p, int64_t B, int64_t ldc)
+{
+    const int64_t ncols = p.epi == QGEMM_EPI_SWIGLU ? p.N / 2 : p.N;
+    return B * ldc > (1ll << 31) - 1 || B * ncols > (1ll << 31) - 1 || (p.L.RT + 1) * 512 > MAX_THREADS;
+}
+
 // The INT8 product of B > 0 rows of codes; `part` (part_bytes) holds the
 // partial tiles of a K split, or null.
 static int i8_product(const qgemm_plan *plan, const I8Args &a, uint8_t *part, int64_t part_bytes, hipStream_t st)
@@ -974,6 +988,9 @@ static int run_with(const qgemm_plan *plan, int64_t B, const void *w, const void
             return fail(QGEMM_ENOTSUP, "qgemm_run: QGEMM_INT8 quantises the rows into a workspace of "
                                        "qgemm_workspace_bytes (qgemm_run_ws or qgemm_run_noalloc), or takes codes "
                                        "(qgemm_run_codes)");
+        if (i8_too_large(p, B, i8_code_stride(p)) || too_many_rows(B, p.K))
+            return fail(QGEMM_EINVAL, "qgemm_run: codes (16 bytes a row at least) or outputs above 2^31 elements, more "
+                                      "rows than one launch takes, or N above 2^27");
         if (i8_tier(plan, B) == QGEMM_TIER_SKINNY && i8_small_fuses(B, p.K, p.L.S)) {
             const hipError_t e = launch_i8_small_fused(i8_args(p, B, w, nullptr, 0, nullptr, y), x, p.act, p.out, st);
             return e == hipSuccess ? QGEMM_OK : hip_fail(e, "qgemm_run: kernel launch");
@@ -1315,7 +1332,7 @@ static int check_rows(const char *who, qgemm_dtype act, int64_t B, int64_t K, co
         return fail(QGEMM_EINVAL, "%s: null pointer", who);
     if (!aligned16(x) || !aligned16(codes) || ((uintptr_t)scales & 3u))
         return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
-    if ((B + 3) * (K <= 1024 ? 64 : K <= 2048 || B > 256 ? 256 : 1024) > MAX_THREADS)
+    if (too_many_rows(B, K))
         return fail(QGEMM_EINVAL, "%s: B=%lld rows of K=%lld are too many for one launch", who, (long long)B,
                     (long long)K);
     return QGEMM_OK;
@@ -1357,9 +1374,8 @@ static int check_codes(const char *who, const qgemm_plan *plan, int64_t B, const
         return fail(QGEMM_EINVAL, "%s: null pointer", who);
     if (!aligned16(codes) || !aligned16(y) || ((uintptr_t)scales & 3u))
         return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
-    const int64_t ncols = p.epi == QGEMM_EPI_SWIGLU ? p.N / 2 : p.N;
-    if (B * ldc > (1ll << 31) - 1 || B * ncols > (1ll << 31) - 1)
-        return fail(QGEMM_EINVAL, "%s: codes or outputs above 2^31 elements", who);
+    if (i8_too_large(p, B, ldc))
+        return fail(QGEMM_EINVAL, "%s: codes or outputs above 2^31 elements, or N above 2^27", who);
     return QGEMM_OK;
 }
 

@@ -610,6 +610,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
         return;
     const int row0 = __builtin_amdgcn_readfirstlane(found[1]);
     const int rows = min(S::BM, __builtin_amdgcn_readfirstlane(found[2]) - row0);
+    if (rows <= 0)
+        return;  // bad offsets whose counts passed 32 bits
     const uint8_t *w = uniform_ptr(grp.wtab[e]);
     TI_LDS(S, lds);
     for (int nt = nt0; nt < min(nt0 + per, ntiles); nt++) {

@@ -114,6 +114,15 @@ def test_run_refusals():
     st, small = _create(4, 1, 1, 0, 2, 16, 16, 1)               # forced to the small-batch tier
     assert codes(small, 16 * 65535 + 1, P16, P16, 16, P16, P16, None, 0, None) == q.EINVAL
     L.qgemm_destroy(small)
+    st, wide = _create(4, 1, 1, 0, 2, 1 << 28, 16, 0)           # workgroups of one launch
+    for B in (1, 4):
+        assert codes(wide, B, P16, P16, 16, P16, P16, None, 0, None) == q.EINVAL
+        assert L.qgemm_run_ws(wide, B, P16, P16, P16, P16, 1 << 40, None) == q.EINVAL
+    L.qgemm_destroy(wide)
+    st, short = _create(4, 1, 1, 0, 2, 1, 1, 0)                 # rows of one element, 16 bytes of codes
+    for B in (1 << 27, 1 << 30):
+        assert L.qgemm_run_ws(short, B, P16, P16, P16, P16, 1 << 40, None) == q.EINVAL
+    L.qgemm_destroy(short)
     assert but(7, P16 + 128) == q.EINVAL                        # workspace alignment
     L.qgemm_destroy(h)
     st, h = _create(0, 0, 0, 0, 0, 256, 512, 0)
