@@ -633,9 +633,10 @@ __global__ __launch_bounds__(64 * S::NW, 2) void i8_grouped_kernel(I8Args a, I8G
 // for each 64 k; that time grows with the workgroups at work, for their share of
 // L2 and of the clock: step[0] with up to 128 of them, step[1] with 256, step[2]
 // with all that the CUs hold.  Choices it makes, with the runner-up: 16 x 5120 x
-// 5120 32x32 7.8 (32x64 8.5); 70 x 5120 x 17408 32x64 28 (64x64 31); 128 x 5120 x
-// 5120 64x64 11.7 (64x128R 14.0); 256: 64x128R 14.7 (64x64 20); 512: 128x128R 21 (64x128 24); 1024:
-// 128x256 32 (64x128 39); 2048: 256x256 55 (128x128R 66).
+// 5120 32x32 7.5 (32x64 8.4); 70 x 5120 x 17408 32x64 28 (128x128R, split, 28;
+// 64x64 31); 128 x 5120 x 5120 64x64 11.2 (64x128R 13.9); 256: 64x128R 14.6
+// (128x128R 19); 512: 128x128R 20 (64x128 24); 1024: 128x256 32 (64x128 39); 2048:
+// 256x256 54 (128x128R 64).
 struct ShapeCost {
     int BM, BN, resident;  // workgroups a CU holds
     float fixed, step[3];
