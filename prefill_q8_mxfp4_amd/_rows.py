@@ -129,7 +129,9 @@ def _codes_addr(codes, dev):
 def _workspace(plan, workspace, B, dev, stream):
     """(address, bytes) of a call's workspace: the caller's, none, or ("auto")
     the plan's, asked for again only when the width, the device or the stream
-    is not the last call's, or a graph is captured."""
+    is not the last eager call's.  A captured call always asks and leaves no
+    answer behind: the plan does not record the capture's stream for it, which
+    the next eager call on that stream has to have done."""
     if workspace is None:
         return 0, 0
     if not isinstance(workspace, str):
@@ -138,10 +140,12 @@ def _workspace(plan, workspace, B, dev, stream):
         return 0, 0
     key = (B, dev, _raw_stream(dev) if stream is None else stream.cuda_stream)
     last = plan.__dict__.get("_ws_last")
-    if last is None or last[0] != key or torch.cuda.is_current_stream_capturing():
+    capturing = torch.cuda.is_current_stream_capturing()
+    if last is None or last[0] != key or capturing:
         st = torch.cuda.current_stream(dev) if stream is None else stream
         ws = plan._workspace(B, torch.device("cuda", dev), st)
-        last = plan._ws_last = (key, ws.data_ptr(), ws.numel())
+        last = (key, ws.data_ptr(), ws.numel())
+        plan._ws_last = None if capturing else last
     return last[1], last[2]
 
 

@@ -1,0 +1,63 @@
+"""The binding of the 8-bit products and the row movements without a GPU: what it
+asks of torch's streams, devices and allocator, and what it hands to the library,
+both replaced by recorders."""
+
+import contextlib
+
+import pytest
+import torch
+
+import prefill_q8_mxfp4_amd as q
+from prefill_q8_mxfp4_amd import _rows
+
+
+class FakeStream:
+    def __init__(self, number, device=0):
+        self.cuda_stream, self.device_index = number, device
+
+    def __repr__(self):
+        return "s%d" % self.cuda_stream
+
+
+class Machine:
+    """Streams and capture state of a machine that is not there."""
+
+    def __init__(self):
+        self.current = FakeStream(1)
+        self.capture = None          # id of the capture that is on
+        self.recorded = []           # (address, stream) of record_stream
+
+
+@pytest.fixture
+def machine(monkeypatch):
+    m = Machine()
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, m.current = m.current, stream
+        yield
+        m.current = before
+
+    cpu = torch.device("cpu")
+    monkeypatch.setattr(torch, "device", lambda *a: cpu)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: m.current)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: m.capture is not None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: m.recorded.append((t.data_ptr(), s)), raising=False)
+    monkeypatch.setattr(_rows, "_raw_stream", lambda dev: m.current.cuda_stream)
+    return m
+
+
+def test_workspace_is_recorded_after_a_capture(machine):
+    """A workspace that a capture took, on a stream other than the one it was made
+    on, is recorded on that stream by the first eager call there: the block must
+    not go back to the allocator while that stream's work on it is pending."""
+    plan = q.Plan("int8", 5120, 5120, act="bf16")
+    s0, st = machine.current, FakeStream(2)
+    at, n = _rows._workspace(plan, "auto", 64, 0, None)
+    assert n >= plan.workspace_bytes(64) and (at, s0) in machine.recorded
+    machine.current, machine.capture = st, 7
+    assert _rows._workspace(plan, "auto", 64, 0, None) == (at, n)
+    machine.capture = None
+    assert _rows._workspace(plan, "auto", 64, 0, None) == (at, n)
+    assert (at, st) in machine.recorded
