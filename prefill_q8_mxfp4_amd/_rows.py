@@ -144,6 +144,8 @@ def _workspace(plan, workspace, B, dev, stream):
     if last is None or last[0] != key or capturing:
         st = torch.cuda.current_stream(dev) if stream is None else stream
         ws = plan._workspace(B, torch.device("cuda", dev), st)
+        if ws is None:  # a width or a plan that the library refuses
+            return 0, 0
         last = (key, ws.data_ptr(), ws.numel())
         plan._ws_last = None if capturing else last
     return last[1], last[2]

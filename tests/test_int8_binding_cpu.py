@@ -61,3 +61,28 @@ def test_workspace_is_recorded_after_a_capture(machine):
     machine.capture = None
     assert _rows._workspace(plan, "auto", 64, 0, None) == (at, n)
     assert (at, st) in machine.recorded
+
+
+def on_gpu(monkeypatch, device=0):
+    """Host tensors pass for tensors of a GPU, which is the current one."""
+    monkeypatch.setattr(_rows, "_gpu", lambda t: device)
+    monkeypatch.setattr(_rows, "_addr", lambda t, name, dev: t.data_ptr())
+    monkeypatch.setattr(_rows, "_codes_addr", lambda t, dev: t.data_ptr())
+    monkeypatch.setattr(_rows, "_current_device", lambda: device)
+
+
+def test_refusals_come_from_the_library(machine, monkeypatch):
+    """Calls for which there is no workspace to ask for reach the library's checks."""
+    on_gpu(monkeypatch)
+    plan = q.Plan("int8", 32, 48, act="bf16", out="bf16")
+    w = torch.zeros(plan.weight_bytes, dtype=torch.uint8)
+    x, y = torch.zeros(4, 48, dtype=torch.bfloat16), torch.zeros(4, 32, dtype=torch.bfloat16)
+    with pytest.raises(q.QgemmError) as e:
+        plan.run(x, w, y, B=-1)
+    assert e.value.status == q.EINVAL
+    plan.close()
+    for call in (lambda: plan.run(x, w, y),
+                 lambda: plan.run_codes(torch.zeros(4, 48, dtype=torch.int8), torch.zeros(4), w, y)):
+        with pytest.raises(q.QgemmError) as e:
+            call()
+        assert e.value.status == q.EINVAL
