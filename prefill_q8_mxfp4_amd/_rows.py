@@ -3,9 +3,18 @@
 
 A call costs a few microseconds of host time, which bounds the small ones, so
 the checks ask the tensors for little, and the raw stream (0.1 us) rather than
-a Stream object (2 us) is taken."""
+a Stream object (2 us) is taken.
+
+`stream` is a torch.cuda.Stream of the tensors' device, the current one if not
+given.  A call on another stream than the current one is ordered against
+nothing else: the caller has it wait for the inputs' producers, keeps tensors
+of other streams alive until it has run (Tensor.record_stream), and has the
+consumers wait for it.  Outputs that a function allocates belong to the stream
+of the call."""
 
 from __future__ import annotations
+
+from contextlib import nullcontext
 
 import torch
 
@@ -17,9 +26,16 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 _OUT = {"f32": torch.float32, "bf16": torch.bfloat16}
 _I32, _F32, _I8, _U8 = torch.int32, torch.float32, torch.int8, torch.uint8
 _LIB = lib()
+_CURRENT = nullcontext()
 
 
 # ------------------------------------------------------------ arguments
+
+def _on(stream):
+    """Where a call's outputs are allocated: they belong to the stream that it
+    is launched on, like tensors made under torch.cuda.stream(stream)."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
 
 def _gpu(t):
     """Index of a tensor's GPU."""
@@ -202,7 +218,8 @@ def pack_int8(codes, scales, out=None, stream=None):
         raise ValueError("scales must be [N]")
     nbytes = weight_bytes("int8", N, K)
     if out is None:
-        out = torch.empty(nbytes, dtype=_U8, device=codes.device)
+        with _on(stream):
+            out = torch.empty(nbytes, dtype=_U8, device=codes.device)
     if out.dtype != _U8 or out.numel() < nbytes:
         raise ValueError("out must be uint8, at least %d bytes" % nbytes)
     dev = _gpu(codes)
@@ -217,10 +234,12 @@ def quantize_rows(x, codes=None, scales=None, stream=None):
     allocated unless given.  Codes at a larger pitch get zeros up to it."""
     dt = _dtype(x, "x")
     B, K = _rows(x, "x")
-    if codes is None:
-        codes = new_codes(B, K, x.device)
-    if scales is None:
-        scales = torch.empty(B, dtype=_F32, device=x.device)
+    if codes is None or scales is None:
+        with _on(stream):
+            if codes is None:
+                codes = new_codes(B, K, x.device)
+            if scales is None:
+                scales = torch.empty(B, dtype=_F32, device=x.device)
     rows, ldc = _codes(codes, scales, K)
     if rows != B:
         raise ValueError("codes must have x's rows")
@@ -240,10 +259,12 @@ def route(ids, E: int, offsets=None, pos=None, stream=None):
     shape = ids.shape
     if ids.dtype != _I32 or len(shape) != 2:
         raise TypeError("ids must be int32 [T][topk]")
-    if offsets is None:
-        offsets = torch.empty(E + 1, dtype=_I32, device=ids.device)
-    if pos is None:
-        pos = torch.empty_like(ids)
+    if offsets is None or pos is None:
+        with _on(stream):
+            if offsets is None:
+                offsets = torch.empty(E + 1, dtype=_I32, device=ids.device)
+            if pos is None:
+                pos = torch.empty_like(ids)
     if offsets.dtype != _I32 or pos.dtype != _I32:
         raise TypeError("offsets and pos must be int32")
     if offsets.numel() != E + 1 or pos.shape != shape:

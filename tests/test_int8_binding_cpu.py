@@ -86,3 +86,37 @@ def test_refusals_come_from_the_library(machine, monkeypatch):
         with pytest.raises(q.QgemmError) as e:
             call()
         assert e.value.status == q.EINVAL
+
+
+def test_outputs_belong_to_the_launch_stream(machine, monkeypatch):
+    """Outputs that the binding allocates for a call on a stream are that stream's
+    blocks: those of the current stream could still be in use there, or be handed
+    out again there while the kernel writes them."""
+    on_gpu(monkeypatch)
+    made, calls = [], []
+    empty, empty_like = torch.empty, torch.empty_like
+
+    def note(f):
+        def made_by(*a, **k):
+            t = f(*a, **k)
+            made.append((t.data_ptr(), machine.current))
+            return t
+        return made_by
+
+    monkeypatch.setattr(torch, "empty", note(empty))
+    monkeypatch.setattr(torch, "empty_like", note(empty_like))
+    monkeypatch.setattr(_rows, "_call", lambda f, dev, stream, *args: calls.append(stream))
+    side = FakeStream(5)
+    x, ids = torch.zeros(4, 48), torch.zeros(4, 2, dtype=torch.int32)
+    weights = torch.zeros(16, 48, dtype=torch.int8), torch.zeros(16)
+    for stream in (None, side):
+        for call in (lambda: q.quantize_rows(x, stream=stream), lambda: q.route(ids, 8, stream=stream),
+                     lambda: (q.pack_int8(*weights, stream=stream),)):
+            outs = call()
+            assert len(made) == len(outs)
+            assert {at for at, _ in made} == {t.data_ptr() for t in outs}
+            assert all(s is (stream or machine.current) for _, s in made), made
+            assert calls == [stream] and machine.current.cuda_stream == 1
+            made.clear(), calls.clear()
+    q.quantize_rows(x, torch.zeros(4, 48, dtype=torch.int8), torch.zeros(4), stream=side)
+    assert not made                                 # given outputs: nothing allocated
