@@ -115,15 +115,18 @@ def new_codes(R, K, device):
     return torch.empty((R, code_stride(K)), dtype=_I8, device=device)[:, :K]
 
 
-def _codes(codes, scales, K):
-    """(rows, pitch) of a tensor of codes, checked with its scales."""
+def _codes(codes, scales, K, written=False):
+    """(rows, pitch) of a tensor of codes, checked with its scales.  Rows that
+    are written get zeros up to their pitch, so that has to be theirs."""
     if codes.dtype != _I8 or scales.dtype != _F32:
         raise TypeError("codes must be int8 and scales float32, not %s and %s" % (codes.dtype, scales.dtype))
     B, cols = _rows(codes, "codes")
     if cols != K:
         raise ValueError("codes must be rows of %d" % K)
     ldc, step = codes.stride()
-    if B <= 1:  # one row, or none, carries no pitch of its own
+    # one row, or none, carries no pitch of its own; one without padding is read
+    # with the bytes behind it, which do not matter, but not written with them
+    if B <= 1 and not (B and written and K % 16 and ldc < code_stride(K)):
         ldc = max(ldc, code_stride(K))
     if (step != 1 and K > 1) or ldc % 16 or ldc < K:
         raise ValueError("codes must be rows of stride 1 at a pitch that is a multiple of 16 and at least K")
@@ -240,7 +243,7 @@ def quantize_rows(x, codes=None, scales=None, stream=None):
                 codes = new_codes(B, K, x.device)
             if scales is None:
                 scales = torch.empty(B, dtype=_F32, device=x.device)
-    rows, ldc = _codes(codes, scales, K)
+    rows, ldc = _codes(codes, scales, K, True)
     if rows != B:
         raise ValueError("codes must have x's rows")
     dev = _gpu(x)
@@ -294,7 +297,7 @@ def dispatch_codes(x, pos, codes, scales, stream=None):
     dt = _dtype(x, "x")
     T, K = _rows(x, "x")
     k = _topk(pos, T)
-    R, ldc = _codes(codes, scales, K)
+    R, ldc = _codes(codes, scales, K, True)
     dev = _gpu(x)
     _call(_LIB.qgemm_dispatch_codes, dev, stream, dt, T, k, K, R, _addr(x, "x", dev), _addr(pos, "pos", dev),
           _codes_addr(codes, dev), ldc, _addr(scales, "scales", dev))

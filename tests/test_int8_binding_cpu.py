@@ -120,3 +120,31 @@ def test_outputs_belong_to_the_launch_stream(machine, monkeypatch):
             made.clear(), calls.clear()
     q.quantize_rows(x, torch.zeros(4, 48, dtype=torch.int8), torch.zeros(4), stream=side)
     assert not made                                 # given outputs: nothing allocated
+
+
+def test_one_row_of_codes_keeps_to_itself(machine, monkeypatch):
+    """Codes are written with zeros up to their pitch.  One row whose own stride has
+    no room for them, a row of a matrix without padding, is refused as an output,
+    like two rows are: the next row begins there.  As an input it is fine."""
+    on_gpu(monkeypatch)
+    pitches = []
+    monkeypatch.setattr(_rows, "_call", lambda f, dev, stream, *args: pitches.append(args))
+    K = 20
+    dense, padded = torch.zeros(4, K, dtype=torch.int8), torch.zeros(4, 48, dtype=torch.int8)
+    x, pos, s = torch.zeros(1, K), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(4)
+    for rows in (1, 2):
+        with pytest.raises(ValueError, match="pitch"):
+            q.quantize_rows(torch.zeros(rows, K), dense[:rows], s)
+    with pytest.raises(ValueError, match="pitch"):
+        q.dispatch_codes(x, pos, dense[:1], s)
+    with pytest.raises(ValueError, match="pitch"):
+        q.quantize_rows(x, torch.zeros(64, dtype=torch.int8)[:K].unsqueeze(0), s)
+    assert not pitches
+    # room of its own: a pitch, or a row that ends on a multiple of 16
+    q.quantize_rows(x, padded[1:2, :K], s)
+    q.quantize_rows(x)
+    q.quantize_rows(torch.zeros(1, 32), dense.view(-1)[:32].unsqueeze(0), s)
+    assert [a[5] for a in pitches] == [48, 32, 32]
+    plan = q.Plan("int8", 32, K, act="bf16", out="f32")
+    plan.run_codes(dense[:1], s, torch.zeros(plan.weight_bytes, dtype=torch.uint8), torch.zeros(1, 32))
+    assert pitches[-1][4] == 32
