@@ -1416,7 +1416,8 @@ int qgemm_run_grouped_codes(const qgemm_plan *plan, int64_t E, int64_t T, const 
         return fail(QGEMM_EHIP, "qgemm_run_grouped_codes: no device status word");
     const I8Args a = i8_args(plan->p, T, nullptr, codes, ldc, scales, y);
     const int forced = plan->p.kn.i8_shape;
-    const int shape = forced == I8_64x128 || forced >= I8_32x128 ? forced : i8_grouped_shape(E, T);
+    const bool routed = forced == I8_64x128 || forced == I8_32x128 || forced == I8_128x128;
+    const int shape = routed ? forced : i8_grouped_shape(E, T);
     // row tiles of 32 at least, weight tiles of 128, 512 threads at most
     if ((T / 32 + (E < T ? E : T) + 8) * ((int64_t)a.RT / 8 + 1) > MAX_THREADS / 512)
         return fail(QGEMM_EINVAL, "qgemm_run_grouped_codes: grid too large");

@@ -116,8 +116,9 @@ struct I8TiCfg {
     int split;           // workgroups along K for each tile
     int64_t part_bytes;  // int32 partial tiles (0 without a split)
 };
-// The shape and K split of least cost; shape, pieces: forced where not 0 (a
-// split only with `split`: room for its partial tiles).
+// The shape and K split of least cost; shape, pieces: forced where they name a
+// shape of dense calls and a positive number (a split only with `split`: room for
+// its partial tiles).
 I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int shape, int pieces);
 hipError_t launch_i8_tiled(const I8Args &a, const I8TiCfg &c, int32_t *part, int outt, hipStream_t st);
 int i8_grouped_shape(int64_t E, int64_t T);

@@ -689,7 +689,7 @@ I8TiCfg i8_tiled_cfg(const I8Args &a, bool split, int shape, int pieces)
         for (int s = 1; s <= 16 && s <= fours; s *= 2) {
             if (s > 1 && (!split || tiles >= 256))
                 break;  // enough workgroups as it is
-            const int want = split && pieces ? (pieces < fours ? pieces : fours) : s;
+            const int want = split && pieces > 0 ? (pieces < fours ? pieces : fours) : s;
             const int per = (fours + want - 1) / want;
             c.split = (fours + per - 1) / per;  // no empty piece
             c.part_bytes = c.split > 1 ? tiles * c.split * p.BM * p.BN * 4 : 0;

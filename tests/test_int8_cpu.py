@@ -272,3 +272,18 @@ def test_binding_refusals():
         q.pack_int8(z(16, 32, dtype=i8), z(15))
     with pytest.raises(ValueError):
         q.pack_int8(z(16, 32, dtype=i8), z(16), z(8, dtype=torch.uint8))
+
+
+def test_knobs_that_name_nothing(monkeypatch):
+    """A number of K pieces below one, or a tile shape there is not, leaves the
+    choice as it is (a negative number of pieces would be a negative grid)."""
+    def sizes():
+        return [q.Plan("int8", N, K, tier="tiled").workspace_bytes(B)
+                for B, N, K in ((20, 64, 17408), (64, 128, 8192), (17, 32, 100000), (70, 5120, 17408))]
+
+    own = sizes()
+    for knob, values in (("QGEMM_TI_SPLIT", ("-1", "-3", "0", "-100000")), ("QGEMM_I8_SHAPE", ("-1", "0", "11", "99"))):
+        for v in values:
+            monkeypatch.setenv(knob, v)
+            assert sizes() == own, (knob, v)
+            monkeypatch.delenv(knob)
