@@ -217,6 +217,15 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _capture_id(stream):
+    """Number of the capture that a stream is part of, no two alike, or None.
+    (The library's handle also finds the HIP runtime that it is linked to.)"""
+    status, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    failed = lib().hipStreamGetCaptureInfo(ctypes.c_void_p(stream.cuda_stream), ctypes.byref(status),
+                                           ctypes.byref(number))
+    return None if failed or status.value != 1 else number.value  # 1: hipStreamCaptureStatusActive
+
+
 def _dev_ptr(t, name):
     import torch
 
@@ -278,21 +287,43 @@ class Plan:
         if need == 0:
             return None
         ws = getattr(self, "_ws", None)
-        if ws is None or ws.numel() < need or ws.device != device:
-            with torch.cuda.stream(stream):
-                ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
-            old = getattr(self, "_ws", None)
-            if old is not None and old.device == device and not torch.cuda.is_current_stream_capturing():
-                old.record_stream(stream)
-            self._ws = ws
+        fits = ws is not None and ws.numel() >= need and ws.device == device
         if torch.cuda.is_current_stream_capturing():
+            if not fits:
+                ws = self._captured_workspace(need, device, stream)
             # replays use this buffer for as long as the plan lives, also
             # after a later call has taken a larger one
             kept = self.__dict__.setdefault("_ws_captured", [])
             if not any(k is ws for k in kept):
                 kept.append(ws)
-        else:
-            ws.record_stream(stream)
+            return ws
+        if not fits:
+            old = ws
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            if old is not None and old.device == device:
+                old.record_stream(stream)
+            self._ws = ws
+        ws.record_stream(stream)
+        return ws
+
+    def _captured_workspace(self, need, device, stream):
+        """The workspace of captured calls wider than any eager one so far.  Its
+        zeroing is a node of the graph and happens when that is replayed, so
+        eager calls never take this buffer, and a further capture zeroes it
+        for itself: its graph may be replayed first.  (INT8 products have no
+        counters in it and need no zeros.)"""
+        import torch
+
+        capture = _capture_id(stream)
+        last, ws = getattr(self, "_ws_graph", (None, None))
+        if ws is None or ws.numel() < need or ws.device != device:
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
+        elif (capture is None or capture != last) and self.fmt != "int8":
+            with torch.cuda.stream(stream):
+                ws.zero_()
+        self._ws_graph = (capture, ws)
         return ws
 
     def run(self, x, w, y, stream=None, B: int | None = None, workspace="auto"):

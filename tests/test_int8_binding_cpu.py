@@ -148,3 +148,31 @@ def test_one_row_of_codes_keeps_to_itself(machine, monkeypatch):
     plan = q.Plan("int8", 32, K, act="bf16", out="f32")
     plan.run_codes(dense[:1], s, torch.zeros(plan.weight_bytes, dtype=torch.uint8), torch.zeros(1, 32))
     assert pitches[-1][4] == 32
+
+
+def test_workspace_made_under_capture(machine, monkeypatch):
+    """A workspace made inside a capture is zeroed by that graph's replays alone.
+    An eager call, which may come before any replay, takes another one; a second
+    capture zeroes it for its own replays, which may come first."""
+    zeroed = []
+    monkeypatch.setattr(q, "_capture_id", lambda stream: machine.capture, raising=False)
+    zero_ = torch.Tensor.zero_
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: zeroed.append(t.data_ptr()) or zero_(t))
+    plan = q.Plan("q8_0", 2048, 1024, act="f32", out="f32")
+    assert plan.workspace_bytes(5) > 0
+
+    def at(B=5, capture=None):
+        machine.capture = capture
+        return plan._workspace(B, torch.device("cuda", 0), machine.current).data_ptr()
+
+    first = at(capture=7)
+    assert at(capture=7) == first and not zeroed     # once for all calls of a capture
+    assert at(capture=8) == first and zeroed == [first]
+    assert at(capture=8) == first and zeroed == [first]
+    eager = at()
+    assert eager != first and at() == eager
+    assert at(capture=9) == eager and zeroed == [first]   # zero since its own first call
+    assert at() == eager
+    kept = {t.data_ptr() for t in plan._ws_captured}
+    assert kept == {first, eager}
+    assert [a for a, _ in machine.recorded] == [eager] * 3
