@@ -64,7 +64,13 @@ def _call(f, dev, stream, *args):
             return _call(f, dev, stream, *args)
         finally:
             torch.cuda.set_device(before)
-    status = f(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if stream is None:
+        raw = _raw_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError("stream must be on the CUDA (HIP) device of the tensors")
+    else:
+        raw = stream.cuda_stream
+    status = f(*args, raw)
     if status != OK:
         _check(status)
 

@@ -176,3 +176,41 @@ def test_workspace_made_under_capture(machine, monkeypatch):
     kept = {t.data_ptr() for t in plan._ws_captured}
     assert kept == {first, eager}
     assert [a for a, _ in machine.recorded] == [eager] * 3
+
+
+def test_stream_of_another_device(machine, monkeypatch):
+    """A stream of another GPU than the tensors' is refused before the call: its
+    kernels would run on that GPU."""
+    on_gpu(monkeypatch, 1)
+    ran = []
+
+    def f(*args):
+        ran.append(args[-1])
+        return q.OK
+
+    _rows._call(f, 1, FakeStream(6, 1), 3)
+    assert ran == [6]
+    with pytest.raises(ValueError, match="stream"):
+        _rows._call(f, 1, FakeStream(6, 0), 3)
+    assert ran == [6]
+
+
+def test_call_on_another_device(monkeypatch):
+    """A call runs with the tensors' GPU as the current one and puts the caller's
+    back, after an error too."""
+    now, seen = [0], []
+    monkeypatch.setattr(_rows, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: now.__setitem__(0, d))
+    monkeypatch.setattr(_rows, "_raw_stream", lambda dev: 100 + dev)
+
+    def f(*args):
+        seen.append((now[0], args))
+        return args[0]
+
+    _rows._call(f, 2, None, q.OK, "x")
+    assert seen == [(2, (q.OK, "x", 102))] and now == [0]
+    with pytest.raises(q.QgemmError):
+        _rows._call(f, 2, None, q.EINVAL)
+    assert now == [0] and seen[-1][0] == 2
+    _rows._call(f, 0, None, q.OK)
+    assert seen[-1] == (0, (q.OK, 100))
