@@ -203,14 +203,15 @@ typedef struct qgemm_plan qgemm_plan;
  * 0 or one QGEMM_FLAG_FORCE_* bit (also settable with the environment
  * variable QGEMM_FORCE_TIER=skinny|tiled|gemv).  Host-only: allocates the small
  * plan object, makes no HIP call and works without a device.  Tuning
- * overrides in the environment (QGEMM_ST_*, QGEMM_SK_*, QGEMM_TI_*) are read
- * here, once.  *plan receives the handle. */
+ * overrides in the environment (QGEMM_ST_*, QGEMM_SK_*, QGEMM_TI_*,
+ * QGEMM_I8_SHAPE) are read here, once.  *plan receives the handle. */
 int qgemm_create(qgemm_plan **plan, qgemm_format fmt, qgemm_dtype act, qgemm_dtype out,
                  qgemm_epilogue epi, qgemm_math math, int64_t N, int64_t K, uint32_t flags);
 
 /* y = x * W^T (or the SwiGLU of the two halves) for B rows.  SwiGLU runs in
  * the small-batch tier for B <= 16 and in the large-batch tier otherwise (a
- * plan forced to the small-batch tier returns QGEMM_ENOTSUP for B > 16).
+ * plan forced to the small-batch tier returns QGEMM_ENOTSUP for B > 16;
+ * QGEMM_INT8 plans take it at any B in either tier).
  *   w: packed weights (device, 16-byte aligned), laid out as above for the
  *      plan's N and K;
  *   x: activations [B][K] row-major (device, 16-byte aligned, act dtype);
@@ -266,7 +267,9 @@ int qgemm_run_grouped(const qgemm_plan *plan, int64_t E, int64_t T, const void *
 int qgemm_grouped_tier(const qgemm_plan *plan, int64_t E, int64_t T);
 
 /* Bytes of device workspace with which qgemm_run_ws may split K across
- * workgroups for this plan and B (0 when the chosen tier does not use one). */
+ * workgroups for this plan and B (0 when the chosen tier does not use one).
+ * For QGEMM_INT8 weights it holds the quantised rows too and is what
+ * qgemm_run_ws needs, at any B > 0. */
 size_t qgemm_workspace_bytes(const qgemm_plan *plan, int64_t B);
 
 /* qgemm_run with a caller-owned workspace (device memory, 256-byte aligned).
@@ -285,7 +288,11 @@ size_t qgemm_workspace_bytes(const qgemm_plan *plan, int64_t B);
  * calls of that plan on the same stream, at any B.  A workspace moved to
  * another plan must be zeroed again.  Calls that may overlap in time need
  * distinct workspaces.  A NULL or smaller workspace selects the unsplit
- * route. */
+ * route.
+ * QGEMM_INT8 plans differ: the rows are quantised into the workspace, so one
+ * that does not hold them (or NULL) returns QGEMM_ENOTSUP, also for the one or
+ * two rows that need not pass through it; with room for the rows but not for
+ * the partial tiles K is not split.  Nothing in it has to be zero. */
 int qgemm_run_ws(const qgemm_plan *plan, int64_t B, const void *w, const void *x, void *y,
                  void *workspace, size_t workspace_bytes, void *stream);
 
@@ -337,7 +344,8 @@ int qgemm_xcd_local(void);
 
 /* Device status word bits: conditions a kernel detected while it ran. */
 #define QGEMM_DEV_XCD_MISMATCH 0x1u /* the K splits of a row group ran on different XCDs */
-#define QGEMM_DEV_BAD_OFFSETS 0x2u  /* qgemm_run_grouped offsets broke their rules; no work done */
+#define QGEMM_DEV_BAD_OFFSETS 0x2u  /* offsets of routed rows broke their rules; no work done (qgemm_run_grouped),
+                                       none for the expert (qgemm_run_grouped_codes) */
 #define QGEMM_DEV_BAD_ROUTE 0x4u    /* a position of a sorted row was past the rows; treated as dropped */
 
 /* Read the current device's status word into *bits (the OR of every bit set

@@ -330,7 +330,9 @@ class Plan:
         """y[B][out_cols] = x[B][K] (x) W; tensors on the GPU, contiguous.
 
         workspace: "auto" (a plan-owned buffer: calls on one plan object must
-        not overlap), None (no K split), or a zero-initialised uint8 tensor."""
+        not overlap), None (no K split), or a zero-initialised uint8 tensor.
+        int8 plans quantise x into it: None, or one below workspace_bytes(B)
+        that has no room for the rows, raises (ENOTSUP); it need not be zero."""
         import torch
 
         if B is None:
@@ -406,7 +408,8 @@ class Plan:
     def run_codes(self, codes, scales, w, y, stream=None, workspace="auto"):
         """qgemm_run_codes: y = the int8 product of rows that are codes
         already (quantize_rows): codes int8 [B][K], rows 16-byte aligned at
-        any pitch; scales float32 [B].  workspace as in run()."""
+        any pitch; scales float32 [B].  workspace as in run(), for a K split
+        alone: None leaves K whole, with the same bits."""
         from . import _rows
 
         return _rows.run_codes(self, codes, scales, w, y, stream, workspace)

@@ -1126,9 +1126,9 @@ int qgemm_run_noalloc(const qgemm_plan *plan, int64_t B, const void *w, const vo
                      need - off > (int64_t)(QGEMM_SCRATCH_BYTES - QGEMM_SCRATCH_COUNTER_BYTES)))
         return fail(QGEMM_EINVAL,
                     "qgemm_run_noalloc: this call needs %lld bytes of scratch (%lld of counters), above "
-                    "the static %lld (%lld); use qgemm_run_ws with a workspace or qgemm_run",
+                    "the static %lld (%lld); use qgemm_run_ws with a workspace or %s",
                     (long long)need, (long long)off, (long long)QGEMM_SCRATCH_BYTES,
-                    (long long)QGEMM_SCRATCH_COUNTER_BYTES);
+                    (long long)QGEMM_SCRATCH_COUNTER_BYTES, plan->p.fmt == FMT_I8 ? "qgemm_run_codes" : "qgemm_run");
     if (need == 0)
         return run_with(plan, B, w, x, y, nullptr, nullptr, 0, (hipStream_t)stream);
     uint8_t *sp = scratch_setup(current_device(), (hipStream_t)stream, false);

@@ -287,3 +287,17 @@ def test_knobs_that_name_nothing(monkeypatch):
             monkeypatch.setenv(knob, v)
             assert sizes() == own, (knob, v)
             monkeypatch.delenv(knob)
+
+
+def test_no_room_in_the_scratch_names_what_takes_the_rows():
+    """Beyond the library's scratch the error names entry points of the format."""
+    L = q.lib()
+    st, h = _create(4, 1, 1, 0, 2, 5120, 17408, 0)
+    assert L.qgemm_run_noalloc(h, 4096, P16, P16, P16, None) == q.EINVAL
+    text = L.qgemm_last_error().decode()
+    assert "qgemm_run_ws" in text and "qgemm_run_codes" in text and "qgemm_run " not in text + " "
+    L.qgemm_destroy(h)
+    st, h = _create(0, 0, 0, 0, 0, 1 << 20, 17408, 0)
+    assert L.qgemm_run_noalloc(h, 16, P16, P16, P16, None) == q.EINVAL
+    assert "qgemm_run " in L.qgemm_last_error().decode() + " "
+    L.qgemm_destroy(h)
