@@ -55,11 +55,13 @@ struct Raw8 {
     }
 };
 
-// Eight codes.  x * (1 / s) is within 2^-15 of the quotient that the definition
-// rounds (|x / s| <= 127.5, three roundings of 2^-23 of it at most), so only a
-// value that near to a border between codes, or one that is no number because
-// 1 / s overflowed, takes the division (ten instructions each: 15.5 against 13.9
-// us for 2048 rows of 5120).
+// Eight codes.  Where 1 / s is finite, s has 22 bits at least (it may be
+// subnormal), |x / s| is below 127.01 and x * (1 / s) within 2^-15 of the quotient
+// that the definition rounds: three roundings of 2^-24 of it.  So only a value
+// within 10^-4 of a border between codes, or one that is no number or infinite
+// because 1 / s overflowed (s of 2^-128 and below, where |x / s| reaches 190),
+// takes the division (ten instructions each: 15.5 against 13.9 us for 2048 rows
+// of 5120).
 __device__ __forceinline__ u32x2 pack_codes8(const float *v, float s, float inv)
 {
     float n[RQ_V];

@@ -4,7 +4,7 @@
 // A step is 64 k.  A packed weight slab is 1 KB in the order in which the lanes
 // of a wave take it, so its load and its read are a contiguous KB each.  Rows of
 // codes are loaded 128 k at a time, whole cache lines (64-byte halves of them,
-// one a step, cost each line twice: 400 against 330 us at 2048 x 34816 x 5120):
+// one a step, cost each line twice: 401 against 345 us at 2048 x 34816 x 5120):
 // a KB holds 8 rows x 128 k, with the eight 16-byte pieces of row r in the order
 // p ^ swizzle(r), so that the 16 lanes that read one k group of 16 rows together
 // find 16 different bank groups.  Nothing is decoded, shuffled or staged in
@@ -796,6 +796,8 @@ static void grouped_go(const I8Args &a, const I8Groups &g, int outt, hipStream_t
 // 48: 93 / 64 / 61 and 88 / 69 / 71; 96: 128 / 98 / 70 and 130 / 97 / 83; of
 // 2048 x 512: mean 8: 33 / 35 / 39 and 32 / 35 / 38; 24: 37 / 40 / 43 and
 // 43 / 40 / 45; 48: 60 / 43 / 48 and 62 / 50 / 52; 96: 93 / 74 / 60 and 90 / 74 / 69.
+// Where the two weights disagree, at means of 8 and 24, the rule follows the one
+// with short K: it gives away 3 to 4 us of 57 there to save 3 to 6 of 33 to 43 here.
 int i8_grouped_shape(int64_t E, int64_t T)
 {
     return T < 16 * E ? I8_32x128 : T < 36 * E ? I8_64x128 : I8_128x128;
