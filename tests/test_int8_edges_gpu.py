@@ -188,3 +188,54 @@ def test_one_row_leaves_the_next_alone():
         q.quantize_rows(x, dense[:1], s)
     torch.cuda.synchronize()
     assert (dense == 9).all()
+
+
+def test_weights_past_four_gigabytes():
+    """2^20 channels of 8192: the last channels lie 8 GB into the packed weights."""
+    N, K, tail = 1 << 20, 8192, 512
+    g = torch.Generator(device=DEV).manual_seed(6)
+    cw = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=DEV, generator=g)
+    sw = torch.rand(N, device=DEV, generator=g) * 1e-3
+    w, last = q.pack_int8(cw, sw), q.pack_int8(cw[-tail:], sw[-tail:])
+    del cw
+    wide, narrow = q.Plan("int8", N, K, act="bf16", out="bf16"), q.Plan("int8", tail, K, act="bf16", out="bf16")
+    for B in (1, 4, 70, 300):
+        x = torch.randn(B, K, device=DEV, generator=g).to(torch.bfloat16)
+        y = wide.run(x, w, torch.empty(B, N, dtype=torch.bfloat16, device=DEV))
+        want = narrow.run(x, last, torch.empty(B, tail, dtype=torch.bfloat16, device=DEV))
+        assert torch.equal(y[:, -tail:], want), B
+
+
+def test_rows_past_four_gigabytes():
+    """140000 sorted rows of 8192 fp32, 4.6 GB: the ends of both sides of each move."""
+    T, k, H = 70000, 2, 8192
+    R = T * k
+    g = torch.Generator(device=DEV).manual_seed(7)
+    pos = torch.arange(R - 1, -1, -1, dtype=torch.int32, device=DEV).view(T, k)  # backwards: token 0 goes last
+    x = torch.randn(T, H, device=DEV, generator=g)
+    xs = q.dispatch(x, pos, torch.empty(R, H, device=DEV))
+    tokens = [0, 1, T // 2, T - 1]
+    for t in tokens:
+        for j in range(k):
+            assert torch.equal(xs[R - 1 - (t * k + j)], x[t]), (t, j)
+    wts = torch.full((T, k), 0.5, device=DEV)
+    y = q.combine(xs, pos, wts, torch.empty(T, H, device=DEV))       # 0.5 x + 0.5 x, exact
+    assert torch.equal(y, x)
+    dys, dw = q.combine_grad(x, xs, pos, wts, torch.zeros(R, H, device=DEV), torch.empty(T, k, device=DEV))
+    for t in tokens:
+        for j in range(k):
+            assert torch.equal(dys[R - 1 - (t * k + j)], 0.5 * x[t]), (t, j)
+    assert torch.equal(dw[:, 0], dw[:, 1])
+    del dys, xs, y
+    codes, scales = torch.empty((R, H), dtype=torch.int8, device=DEV), torch.empty(R, device=DEV)
+    q.dispatch_codes(x, pos, codes, scales)
+    for t in tokens:
+        c, s = q.quantize_rows(x[t:t + 1])
+        for j in range(k):
+            r = R - 1 - (t * k + j)
+            assert torch.equal(codes[r], c[0]) and scales[r] == s[0], (t, j)
+    big = x.repeat(2, 1)                                            # 4.6 GB of rows
+    c, s = q.quantize_rows(big)
+    assert torch.equal(c[:T], c[T:]) and torch.equal(s[:T], s[T:])
+    assert torch.equal(c[0], codes[R - 1]) and s[-1] == scales[0]
+    assert q.device_status() & q.DEV_BAD_ROUTE == 0
