@@ -31,20 +31,24 @@ def test_graphs_captured_before_the_plan_has_run(fmt, act, widths):
     q.init_device(torch.device(DEV))
     want = [warm.run(x, w, torch.empty(x.shape[0], n, device=DEV)) for x in xs]
     torch.cuda.synchronize()
-    graphs, ys = [], []
+    graphs, ys, captures = [], [], []
     for x in reversed(xs):                      # the wide one first: both take its workspace
         y, graph = torch.empty(x.shape[0], n, device=DEV), torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             cold.run(x, w, y)
             cold.run(x, w, y)
+            captures.append(q._capture_id(torch.cuda.current_stream()))
         graphs.insert(0, graph)
         ys.insert(0, y)
+    assert None not in captures and captures[0] != captures[1]
+    assert q._capture_id(torch.cuda.current_stream()) is None
     for rep in range(3):
         for x, graph, y, ref in zip(xs, graphs, ys, want):
             eager = cold.run(x, w, torch.full_like(ref, float("nan")))
             torch.cuda.synchronize()
             assert torch.equal(eager, ref), (rep, x.shape[0])
             y.fill_(float("nan"))
+            cold._ws_graph[1].fill_(255)        # no eager call's: each graph zeroes it for itself
             torch.cuda.synchronize()
             graph.replay()
             torch.cuda.synchronize()
