@@ -369,7 +369,10 @@ hipError_t launch_rms_norm(int dt, int rt, const NormArgs &a, hipStream_t st)
 
 // ---------------------------------------------------------------- gradients
 // With c1 = sum_k h_k^2 and c2 = sum_k dy_k w_k h_k:
-//   dx_k = r dy_k w_k - h_k r^3 c2 / H + dh_k,   dw_k = sum_b dy_k h_k r.
+//   dx_k = r dy_k w_k - (h_k r) (r (r c2 / H)) + dh_k,   dw_k = sum_b dy_k h_k r.
+// In this order every factor is of the size of h r or of dy: r^3 leaves fp32's normal
+// range for rows of 10^13 and larger (a row of 10^15 lost half of its second term) and
+// of 10^-13 and smaller.
 // r comes from h again, which is read anyway.  A workgroup takes every G-th row
 // and keeps its sums of dw in registers; the G partial rows are added, in order,
 // by a second launch.
@@ -470,7 +473,7 @@ __global__ __launch_bounds__(TPR) void rms_norm_grad_kernel(NormGradArgs a)
             c2 += s2[turn][i];
         }
         const float r = 1.f / __builtin_sqrtf(c1 / (float)a.H + a.eps);
-        const float t = r * r * r * (c2 / (float)a.H);
+        const float t = r * (r * (c2 / (float)a.H));
 #pragma unroll
         for (int j = 0; j < NV; j++) {
             const int64_t k = ((int64_t)j * TPR + tid) * NV_E;
@@ -483,8 +486,9 @@ __global__ __launch_bounds__(TPR) void rms_norm_grad_kernel(NormGradArgs a)
                 now.e[j].floats(ev, k, a.H);
 #pragma unroll
             for (int i = 0; i < NV_E; i++) {
-                o[i] = r * (gv[i] * wv[i]) - hv[i] * t + (a.dh ? ev[i] : 0.f);
-                acc[j][i] = fmaf(gv[i], hv[i] * r, acc[j][i]);
+                const float n = hv[i] * r;
+                o[i] = r * (gv[i] * wv[i]) - n * t + (a.dh ? ev[i] : 0.f);
+                acc[j][i] = fmaf(gv[i], n, acc[j][i]);
             }
             if (k < a.H) {
                 if (a.dx)
@@ -506,8 +510,9 @@ __global__ __launch_bounds__(TPR) void rms_norm_grad_kernel(NormGradArgs a)
                 load8<ACT_F32>(a.part, blockIdx.x * a.pitch + k, a.H - k, p);
 #pragma unroll
             for (int i = 0; i < NV_E; i++) {
-                o[i] = r * (gv[i] * wv[i]) - hv[i] * t + (a.dh ? ev[i] : 0.f);
-                p[i] = fmaf(gv[i], hv[i] * r, first ? 0.f : p[i]);
+                const float n = hv[i] * r;
+                o[i] = r * (gv[i] * wv[i]) - n * t + (a.dh ? ev[i] : 0.f);
+                p[i] = fmaf(gv[i], n, first ? 0.f : p[i]);
             }
             if (a.part)
                 store8<ACT_F32, M>(a.part, blockIdx.x * a.pitch + k, a.H - k, p);
