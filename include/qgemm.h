@@ -551,7 +551,8 @@ size_t qgemm_adapt_bytes(int64_t B, int64_t K, int64_t rank);
  * ones.  An adapter whose rank breaks its rules adds nothing, rows of a plan
  * that breaks its rules are left unwritten; both set QGEMM_DEV_BAD_ADAPTER.
  * 8 <= K <= 2^20, 16 <= N <= 2^20.  B = 0 is a no-op.  Deterministic;
- * the order of a row's sums depends on B, K and rank only. */
+ * the order of a row's sums depends on B, K and rank only, so its bits do not
+ * depend on the adapters and ranks of the others. */
 int qgemm_adapt(qgemm_dtype act, qgemm_dtype out, int64_t E, int64_t B, int64_t K, int64_t N, int64_t rank,
                 const void *x, int64_t ldx, const void *const *a_table, const void *const *b_table,
                 const int32_t *ranks, const float *factors, const void *plan, const void *base, int64_t ldb, void *y,

@@ -24,6 +24,8 @@
 // launch 15.8 -> 9.6 us).  Both products in one launch, each workgroup with the
 // tile's sums over all of K for itself, was slower (16 rows: 10.4 against 8.1 us; 70
 // rows, K = 17408: 49 against 12): a CU reads some 27 KB a microsecond so.
+#include <type_traits>
+
 #include "layer.h"
 
 namespace qg {
@@ -494,65 +496,87 @@ __device__ __forceinline__ void up_tile(const AdaptArgs &a, const Tile &t, int r
                 frag[(j * AD_UP + wid) * 64 + lane] = h[j];
     } else {
         // (row tile, 32 ranks) a wave, or two of them, all loads of both in flight; where
-        // there are fewer than waves, the pieces in turn by several waves
-        constexpr int PW = CT * 2 > AD_UP ? CT * 2 / AD_UP : 1;
-        const int parts = CT * KK, by = parts >= AD_UP ? 1 : AD_UP / parts;  // powers of two: KK is 1 or 2
+        // there are fewer than waves, several waves share a lane's eight ranks.  The pieces
+        // are added in order either way: a row's bits do not depend on how many rows its
+        // tile has.
+        const int parts = CT * KK;  // a power of two: KK is 1 or 2
         const float f = a.factors ? a.factors[t.e] : 1.f;
-        auto terms = [&](int i, float *v) {
+        const int64_t step = (int64_t)a.B * a.ldp;
+        // past the rank: of ranks that are there, made zeros by terms()
+        auto place = [&](int part) {
+            const int c = part >> (KK - 1), kk = part & (KK - 1);
+            return a.part + (int64_t)(t.first + min(c * 16 + m, t.n - 1)) * a.ldp + min(kk * 32 + g * 8, rank - 8);
+        };
+        auto terms = [&](int part, float *v) {
+            const bool there = (part & (KK - 1)) * 32 + g * 8 < rank;
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                v[j] *= f;
+                v[j] = there ? v[j] * f : 0.f;
             const Split<NT> sp = split_f32<NT>(v);
 #pragma unroll
             for (int q = 0; q < NT; q++)
-                frag[(((i >> (KK - 1)) * 2 + (i & (KK - 1))) * NT + q) * 64 + lane] = sp.t[q];
+                frag[(((part >> (KK - 1)) * 2 + (part & (KK - 1))) * NT + q) * 64 + lane] = sp.t[q];
         };
-        float v[PW][8];
-        const float *p[PW];
-#pragma unroll
-        for (int w = 0; w < PW; w++) {
-            const int part = (w * AD_UP + wid) & (parts - 1), c = part >> (KK - 1), kk = part & (KK - 1);
-            // past the rank: of ranks that are there, made zeros below
-            p[w] = a.part + (int64_t)(t.first + min(c * 16 + m, t.n - 1)) * a.ldp + min(kk * 32 + g * 8, rank - 8);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                v[w][j] = 0.f;
-        }
-        const int64_t step = (int64_t)a.B * a.ldp;
-#pragma unroll 8
-        for (int s = by == 1 ? 0 : wid >> __builtin_ctz(parts); s < a.split; s += by)
+        if (CT > 2 || parts >= AD_UP) {
+            constexpr int PW = CT * 2 > AD_UP ? CT * 2 / AD_UP : 1;
+            float v[PW][8];
+            const float *p[PW];
 #pragma unroll
             for (int w = 0; w < PW; w++) {
-                const f32x4 lo = *(const f32x4 *)(p[w] + s * step), hi = *(const f32x4 *)(p[w] + s * step + 4);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    v[w][j] += lo[j];
-                    v[w][4 + j] += hi[j];
-                }
-            }
-#pragma unroll
-        for (int w = 0; w < PW; w++) {
-            const int part = (w * AD_UP + wid) & (parts - 1);
-            if ((part & (KK - 1)) * 32 + g * 8 >= rank)
+                p[w] = place((w * AD_UP + wid) & (parts - 1));
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     v[w][j] = 0.f;
-            if (by > 1)
-                __builtin_memcpy(low + (wid * 64 + lane) * 8, v[w], 32);
-            else if (w * AD_UP < parts)
-                terms(part, v[w]);
-        }
-        if (by > 1) {
+            }
+#pragma unroll 8
+            for (int s = 0; s < a.split; s++)
+#pragma unroll
+                for (int w = 0; w < PW; w++) {
+                    const f32x4 lo = *(const f32x4 *)(p[w] + s * step), hi = *(const f32x4 *)(p[w] + s * step + 4);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        v[w][j] += lo[j];
+                        v[w][4 + j] += hi[j];
+                    }
+                }
+#pragma unroll
+            for (int w = 0; w < PW; w++)
+                if (w * AD_UP < parts)
+                    terms(w * AD_UP + wid, v[w]);
+        } else {
+            // W of the eight ranks, eight pieces in flight; those past the last are it
+            // again, and nothing is added of them
+            auto share = [&](auto width) {
+                constexpr int W = decltype(width)::value;
+                const int part = wid & (parts - 1), at = (wid >> (parts - 1)) * W;
+                const float *p = place(part) + at;
+                float v[W];
+#pragma unroll
+                for (int j = 0; j < W; j++)
+                    v[j] = 0.f;
+                for (int s0 = 0; s0 < a.split; s0 += 8) {
+                    uint32_t x[8][W];
+#pragma unroll
+                    for (int s = 0; s < 8; s++)
+                        __builtin_memcpy(x[s], p + min(s0 + s, a.split - 1) * step, 4 * W);
+#pragma unroll
+                    for (int s = 0; s < 8; s++) {
+                        const uint32_t in = s0 + s < a.split ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+                        for (int j = 0; j < W; j++)
+                            v[j] += __uint_as_float(x[s][j] & in);
+                    }
+                }
+                __builtin_memcpy(low + (part * 64 + lane) * 8 + at, v, 4 * W);
+            };
+            if (parts == 1)
+                share(std::integral_constant<int, 2>());
+            else
+                share(std::integral_constant<int, 4>());
             __syncthreads();
             if (wid < parts) {
                 float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    v[j] = 0.f;
-                for (int s = 0; s < by; s++)
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        v[j] += low[((s * parts + wid) * 64 + lane) * 8 + j];
+                __builtin_memcpy(v, low + (wid * 64 + lane) * 8, 32);
                 terms(wid, v);
             }
         }
@@ -648,7 +672,7 @@ template <int OUTT, bool JOINED>
 __global__ __launch_bounds__(64 * AD_UP, OUTT == OUT_BF16 ? 3 : 2) void adapt_up_kernel(AdaptArgs a, int nchunks)
 {
     __shared__ bf16x8 frag[4 * 2 * UpTerms<OUTT>::N * 64];  // 16 or 24 KB
-    __shared__ float low[JOINED ? 1 : AD_UP * 64 * 8];       // 16 KB
+    __shared__ __align__(16) float low[JOINED ? 1 : 2 * 64 * 8];  // 4 KB
     const int n0 = blockIdx.x % nchunks * AD_UP * 64;
     Tile t;
     if (!tile_of(a, blockIdx.x / nchunks, &t, n0 == 0 && threadIdx.x == 0))

@@ -11,25 +11,9 @@ import pytest
 import torch
 
 import prefill_q8_mxfp4_amd as q
+from test_layer_gpu import DEV, DT, HALF, U, Adapters, gen, pick, rows, within
 
 pytestmark = pytest.mark.gpu
-
-U = 2.0 ** -24
-HALF = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8}
-DT = {"f32": torch.float32, "bf16": torch.bfloat16}
-DEV = "cuda:0"
-
-
-def gen(seed):
-    return torch.Generator().manual_seed(seed)
-
-
-def within(got, ref, tol, half=0.0, least=0.0):
-    """|got - ref| <= tol + half |ref| + least everywhere (half covers tol's own part too)."""
-    got, ref = got.double().cpu(), ref.double()
-    assert got.shape == ref.shape
-    off, bound = (got - ref).abs(), tol * (1 + half) + half * ref.abs() + least
-    assert bool((off <= bound).all()), (off / bound.clamp_min(1e-300)).max().item()  # a NaN fails
 
 
 # ------------------------------------------------------------------- norm
@@ -61,3 +45,42 @@ def test_rms_norm_grad_of_large_and_tiny_rows(B, H, dt, rt, size, eps):
     within(dx, ref, tol, HALF[DT[dt]])
     within(dr, ref, tol, HALF[DT[rt]])
     within(dw, dwr, dwt)
+
+
+# --------------------------------------------------------------- adapters
+
+@pytest.mark.parametrize("act,out", [("bf16", "bf16"), ("f32", "f32"), ("codes", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("K,rank,own", [(5120, 16, 16), (2000, 8, 8), (17408, 64, 64), (5120, 64, 40), (5120, 64, 24),
+                                        (800, 48, 32), (5120, 128, 16)])
+def test_adapt_row_alone_and_in_company(K, rank, own, act, out):
+    """A row's bits are the same however many of the others name its adapter, wherever
+    in a tile it stands, whatever ranks the others have."""
+    g = gen(K + rank)
+    B, N, E = 64, 80, 3
+    ad = Adapters(E, K, N, rank, g, [own, rank, 8])
+    x, base = rows(B, K, g), torch.randn(B, N, generator=g).to(DT[out]).to(DEV)
+    if act == "codes":
+        cod, sc = q.quantize_rows(x.to(DEV))
+    else:
+        x = x.to(DT[act]).to(DEV)
+    want = None
+    for n in (1, 2, 15, 16, 17, 31, 32, 33, 63, 64):
+        for at in (0, B - 1, 20):
+            ids = torch.full((B,), -1, dtype=torch.int32)
+            free = [i for i in range(B) if i != at]
+            ids[free[:n - 1] if at else free[64 - n:]] = 0   # rows before and after it
+            ids[[i for i in free if ids[i] < 0][::3]] = 1
+            ids[at] = 0
+            assert (ids == 0).sum() == n
+            plan = q.adapter_rows(ids.to(DEV), E)
+            # the row that is looked at, moved to its place
+            order = torch.tensor([0 if i == at else at if i == 0 else i for i in range(B)], device=DEV)
+            if act == "codes":
+                c = torch.empty(B, q.code_stride(K), dtype=torch.int8, device=DEV)
+                c[:, :K] = cod[order]
+                y = q.adapt_codes(c[:, :K], sc[order], ad.at, ad.bt, rank, plan, base[order], ranks=ad.gr, factors=ad.gf)
+            else:
+                y = ad.run(x[order], plan, base[order])
+            want = y[at].clone() if want is None else want
+            assert torch.equal(y[at], want), (n, at)
+    assert q.device_status(clear=True) == 0
