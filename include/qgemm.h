@@ -452,8 +452,8 @@ int qgemm_combine_grad(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64
  * weight: [H] of type wt, NULL for ones.  The norm is that of h as it is
  * stored.  eps >= 0 and finite; sums are held in fp32, so a row whose squares
  * add up past its range comes out as zeros, and one that holds a NaN or an
- * infinity with NaNs.  h may be residual or x (if the types agree) and y may be
- * x or residual, if h and y are not the same; no other overlap. */
+ * infinity with NaNs.  h may be residual and y may be x; where dt and rt agree h
+ * may be x and y may be residual; h and y are not the same; no other overlap. */
 int qgemm_rms_norm(qgemm_dtype dt, qgemm_dtype rt, qgemm_dtype wt, int64_t B, int64_t H, const void *x,
                    const void *residual, const void *weight, float eps, void *h, void *y, void *stream);
 

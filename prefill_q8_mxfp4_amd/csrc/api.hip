@@ -1612,6 +1612,9 @@ static int norm_call(const char *who, qgemm_dtype dt, qgemm_dtype rt, qgemm_dtyp
         return fail(QGEMM_EINVAL, "%s: misaligned pointer", who);
     if (h && h == y)
         return fail(QGEMM_EINVAL, "%s: h and y are the same buffer", who);
+    // rows of another size: one row's output would lie over others' input
+    if (residual && dt != rt && ((h && h == x) || y == residual))
+        return fail(QGEMM_EINVAL, "%s: h over x, or y over the residual, takes one type of both", who);
     NormArgs a = {};
     a.x = x;
     a.res = residual;
@@ -1674,6 +1677,8 @@ int qgemm_rms_norm_grad(qgemm_dtype dt, qgemm_dtype rt, qgemm_dtype wt, int64_t 
                         qgemm_rms_norm_grad_bytes(B, H));
         if (dx && dx == dr)
             return fail(QGEMM_EINVAL, "qgemm_rms_norm_grad: dx and dr are the same buffer");
+        if (dt != rt && ((dx && (dx == h || dx == dh)) || (dr && dr == dy)))
+            return fail(QGEMM_EINVAL, "qgemm_rms_norm_grad: an output over an input of another type");
     }
     NormGradArgs a = {};
     a.dy = dy;
