@@ -452,7 +452,8 @@ int qgemm_combine_grad(qgemm_dtype dt, int64_t T, int64_t topk, int64_t H, int64
  * weight: [H] of type wt, NULL for ones.  The norm is that of h as it is
  * stored.  eps >= 0 and finite; sums are held in fp32, so a row whose squares
  * add up past its range comes out as zeros, and one that holds a NaN or an
- * infinity with NaNs.  h may be residual and y may be x; where dt and rt agree h
+ * infinity with NaNs; where mean h^2 + eps is below 2^-126 (rows under 10^-19
+ * with as small an eps) squares have lost bits, and y is less exact or no number.  h may be residual and y may be x; where dt and rt agree h
  * may be x and y may be residual; h and y are not the same; no other overlap. */
 int qgemm_rms_norm(qgemm_dtype dt, qgemm_dtype rt, qgemm_dtype wt, int64_t B, int64_t H, const void *x,
                    const void *residual, const void *weight, float eps, void *h, void *y, void *stream);
@@ -477,7 +478,8 @@ size_t qgemm_rms_norm_grad_bytes(int64_t B, int64_t H);
  * Any of dx, dr, dw may be NULL; dx may be dy, dr may be h or dh.  workspace:
  * 16-byte aligned, at least qgemm_rms_norm_grad_bytes(B, H), for dw only;
  * nothing in it has to be zero.  Calls that may overlap in time need distinct
- * ones.  (Where a row's squares add up past fp32, its gradients may be NaN.) */
+ * ones.  (Where a row's squares, or its sum of dy w h, leave fp32, its gradients
+ * may be NaN; mean h^2 + eps below 2^-126 as for qgemm_rms_norm.) */
 int qgemm_rms_norm_grad(qgemm_dtype dt, qgemm_dtype rt, qgemm_dtype wt, int64_t B, int64_t H, const void *dy,
                         const void *h, const void *weight, const void *dh, float eps, void *dx, void *dr, float *dw,
                         void *workspace, size_t workspace_bytes, void *stream);

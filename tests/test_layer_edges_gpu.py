@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import prefill_q8_mxfp4_amd as q
-from test_layer_gpu import DEV, DT, HALF, U, Adapters, gen, pick, rows, within
+from test_layer_gpu import DEV, DT, HALF, U, Adapters, gen, norm_rel, pick, rows, within
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,21 @@ def grad_ref(dy, h, w, eps):
     c = H / 1024 + 50
     tol = U * ((c / 2 + 8) * (r * d * wd).abs() + (2.5 * c + 32) * n.abs() * mt + 3 * ((r * d * wd).abs() + n.abs() * mt))
     return r * d * wd - n * t, tol, (d * n).sum(0), U * (h.shape[0] + 88 + c / 2) * (d * n).abs().sum(0)
+
+
+@pytest.mark.parametrize("size,eps", [(1e16, 1e-6), (1e10, 0.0), (1e-18, 0.0), (1e-18, 1e-37)])
+@pytest.mark.parametrize("B,H", [(3, 64), (5, 521), (2, 24600)])
+def test_rms_norm_of_large_and_tiny_rows(B, H, size, eps):
+    """Rows whose squares add up in fp32 and whose mean square with eps is above 2^-126."""
+    g = gen(H)
+    x, w = torch.randn(B, H, generator=g) * size, 1 + 0.3 * torch.randn(H, generator=g)
+    r = (x.double().square().mean(1, keepdim=True) + eps) ** -0.5
+    y = x.double() * r * w.double()
+    within(q.rms_norm(x.to(DEV), w.to(DEV), eps), y, norm_rel(H) * y.abs())
+    codes, scales = q.rms_norm_codes(x.to(DEV), w.to(DEV), eps)
+    back = codes.double() * scales.double()[:, None]
+    top = y.abs().amax(1, keepdim=True)
+    within(back, y, (0.5 / 127 + 1e-4) * top)   # half a code, and the roundings of the scale
 
 
 @pytest.mark.parametrize("size,eps", [(1e13, 1e-6), (1e14, 1e-6), (1e15, 1e-6), (1e16, 1e-6), (1e-13, 0.0), (1e-14, 1e-35),
