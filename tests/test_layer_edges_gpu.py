@@ -99,3 +99,52 @@ def test_adapt_row_alone_and_in_company(K, rank, own, act, out):
             want = y[at].clone() if want is None else want
             assert torch.equal(y[at], want), (n, at)
     assert q.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["f32", "bf16", "codes"])
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+@pytest.mark.parametrize("B", [1024, 1025, 2100])
+def test_adapt_many_rows(B, rank, act, out):
+    """Rows of a prompt, on both sides of 1024, from where a launch between the two
+    products adds the pieces of K (three of them here); ranks up to the largest, one of 0."""
+    g = gen(B + rank)
+    K, N, E = 1700, 81, 5
+    sizes = [rank, 8, 0, max(8, rank // 16 * 8), rank]
+    ad = Adapters(E, K, N, rank, g, sizes)
+    ad.at[2] = ad.bt[2] = 0
+    ids = pick(B, E, g)
+    plan = q.adapter_rows(ids.to(DEV), E)
+    x, base = rows(B, K, g), torch.randn(B, N, generator=g).to(DT[out])
+    over = base.to(DEV)
+    if act == "codes":
+        c, s = q.quantize_rows(x.to(DEV))
+        x = c.cpu().double() * s.cpu().double()[:, None]
+        args = (c, s, ad.at, ad.bt, rank, plan)
+        y = q.adapt_codes(*args, base.to(DEV), ranks=ad.gr, factors=ad.gf)
+        q.adapt_codes(*args, over, y=over, ranks=ad.gr, factors=ad.gf)
+    else:
+        x = x.to(DT[act])
+        y = ad.run(x.to(DEV), plan, base.to(DEV))
+        ad.run(x.to(DEV), plan, over, y=over)
+    ref, tol = ad.ref(x, ids, base, DT[out])
+    within(y, ref, tol, HALF[DT[out]])
+    still = (ids < 0) | (ids == 2)
+    assert torch.equal(y.cpu()[still], base[still]) and torch.equal(over, y)
+    assert q.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("act,out", [("bf16", "bf16"), ("f32", "f32")])
+def test_adapt_one_piece(act, out):
+    """So many rows that K stays in one piece, ten turns of every wave and an odd end."""
+    g = gen(31)
+    B, K, N, E = 12300, 5123, 40, 3
+    ad = Adapters(E, K, N, 16, g, [16, 8, 16])
+    ids = pick(B, E, g)
+    x, base = rows(B, K, g, DT[act]), torch.randn(B, N, generator=g).to(DT[out])
+    y = ad.run(x.to(DEV), q.adapter_rows(ids.to(DEV), E), base.to(DEV))
+    ref, tol = ad.ref(x, ids, base, DT[out])
+    within(y, ref, tol, HALF[DT[out]])
+    add = ref - base.double()
+    if out == "f32":   # the products' own bound, which does not grow with K
+        assert ((y.cpu().double() - ref).norm(dim=1) <= 1e-5 * add.norm(dim=1) + 1e-6 * base.double().norm(dim=1)).all()
