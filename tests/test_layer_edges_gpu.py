@@ -11,7 +11,9 @@ import pytest
 import torch
 
 import prefill_q8_mxfp4_amd as q
-from test_layer_gpu import DEV, DT, HALF, U, Adapters, gen, norm_rel, pick, rows, within
+from test_layer_gpu import (DEV, DT, EPS, HALF, U, Adapters, choose_ref, gen, grad_choose_ref, norm_ref, norm_rel, pick,
+                            rows, within)
+from test_layer_gpu import grad_ref as ordinary_grad_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +150,74 @@ def test_adapt_one_piece(act, out):
     add = ref - base.double()
     if out == "f32":   # the products' own bound, which does not grow with K
         assert ((y.cpu().double() - ref).norm(dim=1) <= 1e-5 * add.norm(dim=1) + 1e-6 * base.double().norm(dim=1)).all()
+
+
+# -------------------------------------------------------- as they are used
+
+def experts_path(s):
+    """A layer's expert part and its gradients: residual and norm, the choice, rows to
+    their experts and back, each expert a factor of its own on its rows, and all the way
+    back to the norm's input.  Everything that a step gave."""
+    n, h = q.rms_norm(s["x"], s["w"], EPS, residual=s["res"])
+    logits = n.float() @ s["gate"]
+    ids, w = q.choose(logits, 4, score="sigmoid", bias=s["bias"], groups=4, keep=2, best=2, scale=2.5)
+    off, pos = q.route(ids, s["gate"].shape[1])
+    xs = torch.zeros(pos.numel(), n.shape[1], dtype=n.dtype, device=DEV)
+    q.dispatch(n, pos, xs)
+    of_row = torch.bucketize(torch.arange(pos.numel(), device=DEV, dtype=torch.int32), off[1:], right=True)
+    f = s["f"][of_row.clamp_max(s["f"].numel() - 1)][:, None]
+    ys = (xs.float() * f).to(xs.dtype)
+    out = torch.empty_like(n)
+    q.combine(ys, pos, w, out)
+    dys, dw = torch.zeros_like(ys), torch.empty_like(w)
+    q.combine_grad(s["dy"], ys, pos, w, dys, dw)
+    dl = q.choose_grad(logits, ids, dw, score="sigmoid", scale=2.5)
+    dxs = (dys.float() * f).to(dys.dtype)
+    back = torch.empty_like(n)
+    q.dispatch_grad(dxs, pos, back)
+    dn = back + (dl @ s["gate"].t()).to(back.dtype)
+    dx, _, dwn = q.rms_norm_grad(dn, h, s["w"], EPS, dh=s["dy"])
+    return {"n": n, "h": h, "logits": logits, "ids": ids, "w": w, "off": off, "pos": pos, "xs": xs, "ys": ys, "out": out,
+            "dys": dys, "dw": dw, "dl": dl, "dxs": dxs, "back": back, "dn": dn, "dx": dx, "dwn": dwn}
+
+
+def test_layer_gradients_end_to_end():
+    """Each step against 64 bits from what the steps before it stored, forward and back.
+    The experts differ, so that a token's dweights do, and the logits have a gradient."""
+    g = gen(91)
+    B, H, E = 70, 512, 16
+    s = {"x": rows(B, H, g, torch.bfloat16), "res": rows(B, H, g, torch.bfloat16),
+         "w": (1 + 0.1 * torch.randn(H, generator=g)).bfloat16(), "gate": torch.randn(H, E, generator=g) * H ** -0.5,
+         "bias": 0.05 * torch.randn(E, generator=g), "dy": torch.randn(B, H, generator=g).bfloat16(),
+         "f": 0.25 + 1.5 * torch.rand(E, generator=g)}
+    o = {k: v.cpu() for k, v in experts_path({k: v.to(DEV) for k, v in s.items()}).items()}
+    half = HALF[torch.bfloat16]
+    h, _, n = norm_ref(s["x"], s["res"], s["w"])
+    assert torch.equal(o["h"], h)
+    within(o["n"], n, norm_rel(H) * n.abs(), half)
+    ids, w = choose_ref(o["logits"], 4, "sigmoid", s["bias"], 4, 2, 2, True, 2.5)
+    assert torch.equal(o["ids"], ids)
+    args = (2 * o["logits"].double().abs().amax(1, keepdim=True) + 80) * U
+    within(o["w"], w, args * w)
+    pos = o["pos"].long()
+    assert sorted(pos.flatten().tolist()) == list(range(4 * B))
+    for t in range(B):
+        assert torch.equal(o["xs"][pos[t]], o["n"][t].expand(4, H))
+        assert ((pos[t] >= o["off"][ids[t].long()]) & (pos[t] < o["off"][ids[t].long() + 1])).all()
+    w, dy, ys = o["w"].double(), s["dy"].double(), o["ys"].double()[pos]     # [B][4][H]
+    sums = lambda m: (m * w[:, :, None]).sum(1)  # noqa: E731
+    within(o["out"], sums(ys), 8 * U * sums(ys.abs()), half)
+    # back: products and sums in fp32, H of them for dw
+    within(o["dys"][pos], w[:, :, None] * dy[:, None], 2 * U * (w[:, :, None] * dy[:, None]).abs(), half)
+    dot = ys * dy[:, None]
+    within(o["dw"], dot.sum(2), (H + 8) * U * dot.abs().sum(2))
+    dl, mag, own = grad_choose_ref(o["logits"], o["ids"], o["dw"], "sigmoid", True, 2.5)
+    tol = (200 + 2 * o["logits"].double().abs().amax(1, keepdim=True)) * U * mag + own
+    within(o["dl"], dl, tol)
+    assert (dl.abs() > 100 * tol).any(1).all()      # zeros would not pass
+    dxs = o["dxs"].double()[pos]
+    within(o["back"], dxs.sum(1), 8 * U * dxs.abs().sum(1), half)
+    dx, dxt, dwn, dwt = ordinary_grad_ref(o["dn"], o["h"], s["w"], s["dy"])
+    within(o["dx"], dx, dxt, half)
+    within(o["dwn"], dwn, dwt)
+    assert (dx - dy).abs().max() > 0.1 and dwn.abs().max() > 0.1
