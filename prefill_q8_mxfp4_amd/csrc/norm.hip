@@ -589,7 +589,7 @@ static void grad_shape(const NormGradArgs &a, int G, hipStream_t st)
         grad_go<DT, RT, 256, 1>(a, G, st);
     else if (a.H <= 256 * NV_E * 3)
         grad_go<DT, RT, 256, 3>(a, G, st);
-    else if (DT == ACT_BF16 && RT == ACT_BF16)
+    else if constexpr (DT == ACT_BF16 && RT == ACT_BF16)
         grad_go<DT, RT, 512, 5>(a, G, st);
     else  // what five vectors of fp32 take, registers do not have
         grad_go<DT, RT, 512, 4>(a, G, st);
