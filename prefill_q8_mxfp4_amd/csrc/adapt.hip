@@ -22,8 +22,8 @@
 // So nothing else may wait: operands come through unconditional loads (branches
 // around them made each wait for itself: 64 rows of one adapter, rank 16, the second
 // launch 15.8 -> 9.6 us).  Both products in one launch, each workgroup with the
-// tile's sums over all of K for itself, was slower (16 rows: 10.4 against 8.1 us; 70
-// rows, K = 17408: 49 against 12): a CU reads some 27 KB a microsecond so.
+// tile's sums over all of K for itself, was slower (16 rows: 10.4 against 8.1 us, 7.4 by
+// now; 70 rows, K = 17408: 49 against 12): a CU reads some 27 KB a microsecond so.
 #include <type_traits>
 
 #include "layer.h"
@@ -182,7 +182,7 @@ __device__ __forceinline__ void down_tile(const AdaptArgs &a, const Tile &t, int
     }
     // the partial turn of the row's end: vectors that would pass it are the row's last
     // eight elements, those of the vector before made zeros on both sides (loads in
-    // branches would each wait for themselves: K = 5119 took 10.2 us where 5120 takes 7.9)
+    // branches would each wait for themselves: K = 5119 took 10.2 us where 5120 took 7.9)
     k = k0 + ((k1 - k0) & ~63);
     if (k < k1 && ((k - k0) >> 6) % AD_WAVES == wid) {
         bf16x8 w[2][RT];
@@ -666,8 +666,8 @@ __device__ __forceinline__ void copy_tile(const AdaptArgs &a, const Tile &t, int
     }
 }
 
-// Three waves a SIMD with bf16 outputs: at two, 64 rows of 32 adapters take 10.8 us
-// instead of 8.9.
+// Three waves a SIMD with bf16 outputs, which 142 and 154 registers give without being
+// asked; the bound keeps it so (at two, 64 rows of 32 adapters took 10.8 us instead of 8.9).
 template <int OUTT, bool JOINED>
 __global__ __launch_bounds__(64 * AD_UP, OUTT == OUT_BF16 ? 3 : 2) void adapt_up_kernel(AdaptArgs a, int nchunks)
 {
@@ -692,8 +692,9 @@ __global__ __launch_bounds__(64 * AD_UP, OUTT == OUT_BF16 ? 3 : 2) void adapt_up
 // Pieces of K, by B alone: how many adapters the rows name is known on the device
 // only.  Every piece is read again by the second product, so pieces are no smaller
 // than 768 elements (5120 x 5120, all launches; 16 rows of as many adapters of rank
-// 16: 8.3 us at 256, 7.9 at 768, 8.4 at 1536; 64 rows of 32: 11.8, 8.9, 9.4; 64 rows of
-// one of rank 64: 22.6, 18.3, 22.2), and there are fewer of them where the rows make
+// 16: 9.3 us at 256, 7.5 at 768, 8.2 at 1536; 64 rows of 32: 13.1, 9.1, 9.9; 64 rows of
+// one of rank 64: 22.2, 17.9, 21.8; but 16 rows of K = 17408: 17.6, 11.3, 9.5, 70 in fp32
+// 19.0, 13.6, 11.4), and there are fewer of them where the rows make
 // enough tiles for the chip (4096 rows of rank 16: 38.3 us at 512, 36.9 at 768, 33.6
 // at 1536; 2048 rows of rank 64: 35.4, 31.2, 33.9, and 31.6 at 1024, the choice).
 void adapt_shape(AdaptArgs &a)
@@ -708,8 +709,9 @@ void adapt_shape(AdaptArgs &a)
 
 // Whether a launch between the two products adds the pieces up: many rows, whose up
 // workgroups would each add their tile's again (2048 rows, 5120 x 5120 at rank 64:
-// 33.6 us without, 31.8 with; 5120 x 17408 at rank 16: 47.6 and 40.5; 512 rows at
-// rank 16: 14.6 and 15.8), and ranks that a workgroup does not hold at once.
+// 33.7 us without, 31.5 with; 5120 to 17408 at rank 16: 53.2 and 51.8, but 17408 to 5120
+// 40.5 and 44.2; 512 rows of eight at rank 16: 15.4 and 17.2, 1000 18.4 and 19.8), and
+// ranks that a workgroup does not hold at once.
 static bool adapt_joins(int64_t B, int64_t rank) { return rank > AD_CHUNK || B > 1024; }
 
 int64_t adapt_part_bytes(int64_t B, int64_t K, int64_t rank)

@@ -14,7 +14,10 @@
 // the largest key holds the lowest index.  A row is read once; the bytes are few,
 // the time is a wave's chain of steps: 2048 tokens of 512 fp32 logits take 3.5 us for
 // the best one, 5.0 for ten (a maximum over the wave each), 7.7 for ten by sigmoid,
-// bias and groups; 8192 tokens, which fill the vector units, 5.6, 8.7 and 15.4.
+// bias and groups; 8192 tokens, which fill the vector units, 5.6, 8.7 and 15.4.  Of more
+// than 512 experts every key is made in 64 bits where there is a bias or sums of scores,
+// and 32 experts a lane take 124 bytes of scratch: 2048 tokens, sigmoid, bias and groups,
+// top 10, of 1024 experts 17.0, of 2048 36.1 (the best eight logits: 6.8 and 14.9).
 #include <type_traits>
 
 #include "layer.h"

@@ -340,6 +340,12 @@ static void norm_go(const NormArgs &a, hipStream_t st)
         hipLaunchKernelGGL((rms_norm_kernel<DT, RT, CODES, TPR, NV, TPR == 64 ? ROW_TINY : ROW_RAGGED>), g, blk, 0, st, a);
 }
 
+// Rows of 8193 and more: three vectors a thread are more than 128 registers hold beside
+// the next row's unless both types are bf16; 40 to 116 bytes a lane go to scratch there,
+// 12 of ragged bf16 rows (600 x 17408 with a residual: bf16 15.8 us, bf16 with fp32 35.5,
+// fp32 44.6, its codes 51.6, where their bytes take 16.4, 24.7, 32.9 and 26.7; 17407 fp32
+// 58.5).  Rows up to 1024 take a wave whatever their length, so short ones leave lanes
+// idle (81920 x 128 bf16 without a residual: 23.7 us, its bytes 8.3).
 template <int DT, int RT, bool CODES>
 static void norm_shape(const NormArgs &a, hipStream_t st)
 {
@@ -379,7 +385,8 @@ hipError_t launch_rms_norm(int dt, int rt, const NormArgs &a, hipStream_t st)
 // Workgroups: a row of them in flight for every CU, more of short rows, as long as
 // their partial rows of dw are few bytes beside the rows (2048 rows of 5120 in bf16,
 // both launches: 22.7 us with 256, 25.8 with 512, 34.7 with 1024; 8192 rows of 1024: 35.8,
-// 25.8, 21.8).
+// 25.8, 21.8).  Always 256 threads and a barrier a row: short rows leave most idle
+// (81920 x 128 in bf16: 139 us, its bytes 12).
 static int norm_grad_groups(int64_t B, int64_t H)
 {
     // at least two rows each, where there are enough of them
@@ -593,6 +600,8 @@ static void grad_shape(const NormGradArgs &a, int G, hipStream_t st)
         grad_go<DT, RT, 512, 5>(a, G, st);
     else  // what five vectors of fp32 take, registers do not have
         grad_go<DT, RT, 512, 4>(a, G, st);
+    // (ragged rows of more than 6144 do not fit either: 140 to 440 bytes a lane go to scratch;
+    // 512 x 17407: bf16 36.8 us, fp32 71.0, where 17408 take 25.7 and 39.0)
 }
 
 hipError_t launch_rms_norm_grad(int dt, int rt, NormGradArgs a, hipStream_t st)
